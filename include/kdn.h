@@ -49,7 +49,9 @@ typedef enum kdn_status {
   KDN_ERR_CUDA = 5          /* the CUDA runtime reported an error           */
 } kdn_status;
 
-typedef enum kdn_dtype { KDN_F32 = 0, KDN_BF16 = 1 } kdn_dtype;
+/* KDN_E4M3 (8 bits, with fp32 scales: see kdn_fp8_quantize) is an output type
+ * of kdn_rmsnorm_forward only; every other dtype argument takes the first two. */
+typedef enum kdn_dtype { KDN_F32 = 0, KDN_BF16 = 1, KDN_E4M3 = 2 } kdn_dtype;
 typedef enum kdn_variant { KDN_ISO = 0, KDN_DIAG = 1 } kdn_variant;
 
 /* Forward-path selector (the `chunk` argument of the forward calls). */
@@ -63,7 +65,8 @@ enum {
 const char* kdn_status_string(kdn_status status);
 
 /* Library version, major*10000 + minor*100 + patch (0.2.0: adds the packed,
- * host-buffer, backward, dense-filter and KLA entry points). */
+ * host-buffer, backward, dense-filter and KLA entry points; 0.3.0: the gated
+ * linear recurrence, the residual RMS norm and the 8-bit projections). */
 int kdn_version(void);
 
 /* ------------------------------------------------------------------------
@@ -452,6 +455,203 @@ kdn_status kdn_kla_forward_ws(const void* q, const void* k, const void* v,
                               float* lam_out, int B, int T, int H, int dk,
                               int dv, void* workspace, size_t workspace_bytes,
                               void* stream);
+
+/* ------------------------------------------------------------------------
+ * kdn_linear_scan_forward -- the gated linear recurrence, per channel:
+ *     h_t = a_t h_{t-1} + b_t x_t,   y_t = h_t
+ * (forget gate a, write gate b), in fp32, over B sequences of T steps, or over
+ * packed sequences of mixed length.  It is the affine mean recursion that the
+ * information-form filter runs given its gates ("Kalman Linear Attention:
+ * Parallel Bayesian Filtering ...", 方法论 §2), as a layer of its own with one
+ * state per channel; the steps compose by an associative scan, one pass over
+ * the data.
+ *
+ * a        [B, T, D] gate_dtype device: any values (a forget gate is in [0, 1])
+ * b        [B, T, D] gate_dtype device, or NULL for ones
+ * x        [B, T, D] in_dtype device
+ * h0       [B, D] fp32 device initial states, or NULL for zeros
+ * cu_seqlens  NULL, or [B + 1] int32 device: then B sequences are packed in T
+ *          steps, all arrays [B, T, D] are [T, D], and sequence s is steps
+ *          [cu_seqlens[s], cu_seqlens[s + 1]); cu_seqlens[0] = 0,
+ *          non-decreasing, cu_seqlens[B] <= T.  Steps from cu_seqlens[B] on
+ *          are padding: their outputs are left as they were.  Sequences may be
+ *          empty.  Offsets out of order or out of range touch no memory
+ *          outside the arrays; they give unspecified values and
+ *          KDN_ERR_INVALID_ARG from kdn_read_workspace_status.
+ * y        [B, T, D] in_dtype device output (fp32 states, rounded once)
+ * h_out    [B, D] fp32 device final states (an empty sequence's is its initial
+ *          one); may alias h0
+ * workspace   device scratch of >= kdn_linear_scan_workspace_size(B, T, D)
+ *          bytes (packed: B = 1), 256-byte aligned; the call clears what it
+ *          needs first.  Calls that may overlap need a workspace each.
+ * B, D >= 1; T >= 0; every other pointer 16-byte aligned; y must not overlap
+ * the inputs.
+ * Errors: KDN_ERR_INVALID_ARG, KDN_ERR_UNSUPPORTED (more than 2^31 tiles),
+ * KDN_ERR_WORKSPACE, KDN_ERR_CUDA; kdn_read_workspace_status() reports a
+ * bounded wait that gave up, or bad offsets.
+ * ---------------------------------------------------------------------- */
+size_t kdn_linear_scan_workspace_size(int B, int T, int D);
+kdn_status kdn_linear_scan_forward(const void* a, const void* b,
+                                   kdn_dtype gate_dtype, const void* x,
+                                   kdn_dtype in_dtype, const float* h0,
+                                   const int32_t* cu_seqlens, void* y,
+                                   float* h_out, int B, int T, int D,
+                                   void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/* ------------------------------------------------------------------------
+ * kdn_linear_scan_backward -- the gradients of kdn_linear_scan_forward.  With
+ * c the gradient that reaches the state after step t from later steps (dh_T
+ * behind the last step of a sequence), from the last step to the first:
+ *     g = dy_t + c;  dx_t = b_t g;  db_t = x_t g;  da_t = g h_{t-1};  c = a_t g
+ * and dh0 = c before the first step.  h_{t-1} is read from y as it is stored
+ * (h0 before the first step), so with bf16 y it is the rounded state.
+ *
+ * a, b, x, h0, cu_seqlens, B, T, D, workspace: as the forward call (x is read
+ *          only when b is given, and may be NULL otherwise)
+ * y        [B, T, D] in_dtype device: the forward's output
+ * dy       [B, T, D] in_dtype device: dL/dy
+ * dh_T     [B, D] fp32 device: dL/dh_out, or NULL for zeros
+ * da, db   [B, T, D] gate_dtype device outputs (db only with b)
+ * dx       [B, T, D] in_dtype device output
+ * dh0      [B, D] fp32 device output; may alias dh_T
+ * The outputs must not overlap the inputs.  Padding steps are left as they
+ * were.  Errors: as the forward call.
+ * ---------------------------------------------------------------------- */
+kdn_status kdn_linear_scan_backward(const void* a, const void* b,
+                                    kdn_dtype gate_dtype, const void* x,
+                                    const void* y, const void* dy,
+                                    kdn_dtype in_dtype, const float* h0,
+                                    const float* dh_T,
+                                    const int32_t* cu_seqlens, void* da,
+                                    void* db, void* dx, float* dh0, int B,
+                                    int T, int D, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * kdn_linear_scan_step -- one step for B x D channels, the state updated in
+ * place: h <- a h + b x, y = h (the same update as one step of the forward).
+ * a, b     [B, D] gate_dtype device (b or NULL);  x, y [B, D] in_dtype device
+ * h        [B, D] fp32 device, read and overwritten
+ * B, D >= 1; pointers 16-byte aligned.  Errors: KDN_ERR_INVALID_ARG,
+ * KDN_ERR_CUDA.
+ * ---------------------------------------------------------------------- */
+kdn_status kdn_linear_scan_step(const void* a, const void* b,
+                                kdn_dtype gate_dtype, const void* x,
+                                kdn_dtype in_dtype, float* h, void* y, int B,
+                                int D, void* stream);
+
+/* ------------------------------------------------------------------------
+ * kdn_rmsnorm_forward -- the residual addition and root-mean-square norm
+ * around a mixing layer, over rows of D:
+ *     h = x + residual (rounded to residual_dtype; h = x without a residual)
+ *     y = h / sqrt(mean(h^2) + eps) * weight
+ * x takes the fp32 output of the mixing calls as it is; y is bf16 or fp32, or
+ * e4m3 codes with a scale for each 128 of a row, as kdn_fp8_quantize gives and
+ * kdn_fp8_matmul takes.  The norm reads h as it is stored.
+ *
+ * x        [rows, D] x_dtype device
+ * residual [rows, D] residual_dtype device, or NULL
+ * weight   [D] fp32 device
+ * h        [rows, D] residual_dtype device output with a residual (may alias
+ *          residual); NULL without
+ * y        [rows, D] y_dtype device output; e4m3: rows ldy bytes apart, ldy a
+ *          multiple of 16 and at least D (the bytes between D and the next
+ *          multiple of 8 are overwritten).  ldy is not read otherwise.
+ * scale    [rows, ceil(D / 128)] fp32 device output, e4m3 only
+ * eps      >= 0, finite
+ * Sums in fp32: |h| up to about 1e18.  rows >= 0 (0: nothing is done);
+ * 1 <= D <= 16384; pointers 16-byte aligned.  Errors: KDN_ERR_INVALID_ARG,
+ * KDN_ERR_UNSUPPORTED, KDN_ERR_CUDA.
+ * ---------------------------------------------------------------------- */
+kdn_status kdn_rmsnorm_forward(const void* x, kdn_dtype x_dtype,
+                               const void* residual, kdn_dtype residual_dtype,
+                               const float* weight, void* h, void* y,
+                               kdn_dtype y_dtype, int64_t ldy, float* scale,
+                               int64_t rows, int D, float eps, void* stream);
+
+/* ------------------------------------------------------------------------
+ * kdn_rmsnorm_backward -- the gradients of kdn_rmsnorm_forward.  With
+ * rs = 1 / sqrt(mean(h^2) + eps) and dh what reaches h from its other use:
+ *     d = dh + rs (dy weight - h rs^2 mean(dy weight h))
+ *     dx = d,  dresidual = d,  dweight = sum over rows of dy h rs
+ * dx in fp32 is the dO that kdn_backward takes.  For e4m3 outputs dy is the
+ * gradient with respect to the values that codes and scales stand for (the
+ * rounding itself is passed straight through).
+ *
+ * h        [rows, D] h_dtype device: the forward's h (x without a residual)
+ * dy       [rows, D] dy_dtype device
+ * dh       [rows, D] h_dtype device, or NULL for zeros
+ * dx       [rows, D] dx_dtype device output
+ * dresidual  [rows, D] h_dtype device output, or NULL; may alias dh
+ * dweight  [D] fp32 device output (zeros when rows = 0)
+ * workspace   device scratch of >= kdn_rmsnorm_backward_workspace_size(...)
+ *          bytes, 256-byte aligned: the blocks' parts of dweight, added in a
+ *          fixed order.  Calls that may overlap need a workspace each.
+ * Other conditions and errors as the forward, plus KDN_ERR_WORKSPACE.
+ * ---------------------------------------------------------------------- */
+size_t kdn_rmsnorm_backward_workspace_size(int64_t rows, int D);
+kdn_status kdn_rmsnorm_backward(const void* h, kdn_dtype h_dtype,
+                                const float* weight, const void* dy,
+                                kdn_dtype dy_dtype, const void* dh, void* dx,
+                                kdn_dtype dx_dtype, void* dresidual,
+                                float* dweight, int64_t rows, int D, float eps,
+                                void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/* ------------------------------------------------------------------------
+ * kdn_fp8_quantize -- a matrix into e4m3 codes with fp32 scales:
+ *     scale = max(largest magnitude of the block, 2^-100) / 448
+ *     code  = e4m3(value / scale), to nearest, ties to even
+ * A block is 128 values along a row of the output (the last one may be
+ * shorter), or with `tile` a 128 x 128 tile of it.  `transpose` quantises the
+ * transpose of x.  An infinity or NaN in a block makes its scale infinite or
+ * NaN, and so every product with the block NaN.
+ *
+ * x        [rows, cols] x_dtype device
+ * q        e4m3 codes, device output: R rows of C bytes, ldq bytes apart, with
+ *          (R, C) = (rows, cols), or (cols, rows) with transpose; ldq a
+ *          multiple of 16 and at least C (the bytes between C and the next
+ *          multiple of 16 may be overwritten)
+ * scale    [R, ceil(C / 128)] fp32 device output; with tile
+ *          [ceil(R / 128), ceil(C / 128)]
+ * rows >= 0 (0: nothing is done), cols >= 1; x and q 16-byte aligned.
+ * Errors: KDN_ERR_INVALID_ARG, KDN_ERR_UNSUPPORTED (2^31 blocks),
+ * KDN_ERR_CUDA.
+ * ---------------------------------------------------------------------- */
+kdn_status kdn_fp8_quantize(const void* x, kdn_dtype x_dtype, int64_t rows,
+                            int64_t cols, int tile, int transpose, void* q,
+                            int64_t ldq, float* scale, void* stream);
+
+/* ------------------------------------------------------------------------
+ * kdn_fp8_matmul -- the 8-bit projection out = x w^T: x [M, K] and w [N, K] in
+ * e4m3, with a scale for each block of 128 along K,
+ *     out[m, n] = sum_b x_scale[m, b] w_scale[n', b] sum_{k in b} x[m, k] w[n, k]
+ * with n' = n / 128 (w_tile, a weight's 128 x 128 tiles) or n.  It makes the
+ * q, k, v (bf16) and gate inputs (fp32) of the mixing calls from
+ * kdn_rmsnorm_forward's 8-bit output.  With quantised transposes it is also
+ * the backward pass: dx = dy w is the product of dy and w^T (tiles), and
+ * dw = dy^T x the product of dy^T and x^T (rows of 128 tokens, w_tile = 0).
+ * Block products on the tensor cores, exact products, fp32 sums; the sum over
+ * blocks in fp32, in an order that depends only on the sizes and the device.
+ *
+ * x        e4m3 codes, M rows of K bytes, ldx bytes apart
+ * x_scale  [M, ceil(K / 128)] fp32 device
+ * w        e4m3 codes, N rows of K bytes, ldw bytes apart
+ * w_scale  [ceil(N / 128), ceil(K / 128)] (w_tile) or [N, ceil(K / 128)] fp32
+ * out      [M, N] out_dtype device output; must not overlap the inputs
+ * status   one device word or NULL.  Not cleared: a bounded on-device wait
+ *          that gives up (it cannot in correct use) sets it, and
+ *          kdn_read_workspace_status(status, 4, stream) reports it, so zero it
+ *          once before the first call
+ * M >= 0 (0: nothing is done), N, K >= 1; ldx, ldw multiples of 16 and at
+ * least K; x, w, out 16-byte aligned.  Bytes behind K are not read as values.
+ * Errors: KDN_ERR_INVALID_ARG, KDN_ERR_UNSUPPORTED (2^31 tiles), KDN_ERR_CUDA.
+ * ---------------------------------------------------------------------- */
+kdn_status kdn_fp8_matmul(const void* x, int64_t ldx, const float* x_scale,
+                          const void* w, int64_t ldw, const float* w_scale,
+                          int w_tile, void* out, kdn_dtype out_dtype, int M,
+                          int N, int K, uint32_t* status, void* stream);
 
 /* ------------------------------------------------------------------------
  * kdn_read_workspace_status -- synchronise `stream`, then report the device

@@ -1,0 +1,119 @@
+// e4m3 blocks of 128 with one fp32 scale: value = code * scale,
+//   scale = max(amax, 2^-100) / 448,  code = e4m3(value / scale).
+// 448 is the largest e4m3 number, so a block's largest value uses the whole
+// range; the floor keeps a block of zeros from dividing by zero.  An infinity
+// or NaN in a block makes its scale infinite or NaN (the maximum propagates
+// NaN), which marks every product of that block instead of hiding it.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "kdn_common.cuh"
+
+namespace kdn {
+
+constexpr float kE4m3Max = 448.f;
+constexpr float kAmaxFloor = 7.8886090522101181e-31f;  // 2^-100
+
+// the larger of two numbers, NaN if one is
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float fp8_scale(float amax) {
+  return max_nan(amax, kAmaxFloor) / kE4m3Max;
+}
+// what a value is multiplied with for its code: 1 / scale from the maximum
+// itself, so that the quotient carries two roundings, not three
+__device__ __forceinline__ float fp8_inverse(float amax) {
+  return kE4m3Max / max_nan(amax, kAmaxFloor);
+}
+// four codes of v * inv, the first in the lowest byte
+__device__ __forceinline__ uint32_t fp8_pack4(float v0, float v1, float v2, float v3, float inv) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v0 * inv, v1 * inv), __NV_SATFINITE,
+                                               __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v2 * inv, v3 * inv), __NV_SATFINITE,
+                                               __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+// Eight consecutive elements from `p`: `n` of them exist (the others read as
+// 0).  vec: p is 16-byte aligned and all eight exist or none do.
+__device__ __forceinline__ void load8(const float* p, int n, bool vec, float (&v)[8]) {
+  if (vec) {
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+    if (n > 0) {
+      a = __ldg(reinterpret_cast<const float4*>(p));
+      b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    }
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? __ldg(p + i) : 0.f;
+  }
+}
+__device__ __forceinline__ void unpack_bf16x8(const uint4& a, float (&v)[8]) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, int n, bool vec, float (&v)[8]) {
+  if (vec) {
+    uint4 a = make_uint4(0u, 0u, 0u, 0u);
+    if (n > 0) a = __ldg(reinterpret_cast<const uint4*>(p));
+    unpack_bf16x8(a, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? __bfloat162float(p[i]) : 0.f;
+  }
+}
+__device__ __forceinline__ void store8(float* p, int n, bool vec, const float (&v)[8]) {
+  if (vec) {
+    if (n > 0) {
+      reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = v[i];
+  }
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, int n, bool vec, const float (&v)[8]) {
+  if (vec) {
+    if (n > 0) {
+      uint4 a;
+      __nv_bfloat162 h[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      a.x = *reinterpret_cast<uint32_t*>(&h[0]);
+      a.y = *reinterpret_cast<uint32_t*>(&h[1]);
+      a.z = *reinterpret_cast<uint32_t*>(&h[2]);
+      a.w = *reinterpret_cast<uint32_t*>(&h[3]);
+      *reinterpret_cast<uint4*>(p) = a;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = __float2bfloat16_rn(v[i]);
+  }
+}
+__device__ __forceinline__ float amax8(const float (&v)[8]) {
+  float m = fabsf(v[0]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(v[i]));
+  return m;
+}
+// the maximum over this thread's half warp (16 threads hold one block of 128)
+__device__ __forceinline__ float half_warp_max(float m) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+
+}  // namespace kdn

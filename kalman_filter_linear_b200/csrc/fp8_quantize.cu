@@ -1,0 +1,164 @@
+// kdn_fp8_quantize: a matrix into e4m3 codes with one fp32 scale for each 128
+// of a row (activations) or each 128 x 128 tile (weights), as it lies or
+// transposed (the operands of a projection's gradients: dX = dY W needs W's
+// transpose, dW = dY^T X both factors').  fp8_common.cuh has the scale.
+//
+// Rows as they lie: a half warp a block of 128, eight elements a thread, one
+// read and one write.  Tiles and transposes: one block of 256 threads a 128 x
+// 128 tile; a thread holds an 8 x 8 piece, so eight codes of a column are one
+// 8-byte word of the transposed tile.  The words go through shared memory with
+// their position in the row XORed by the piece's column, which keeps the
+// column-wise stores free of bank conflicts, and leave as 16-byte stores.
+#include "fp8_common.cuh"
+
+namespace kdn {
+namespace {
+
+template <typename XT>
+__global__ void __launch_bounds__(256)
+fp8_rows_kernel(const XT* __restrict__ X, uint8_t* __restrict__ Q, float* __restrict__ S,
+                int64_t rows, int C, int64_t ldq, int kb, int vec) {
+  // unit: 8 elements of the row padded to whole blocks
+  const int64_t unit = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t row = unit / (16 * kb);
+  if (unit / 16 >= rows * kb) return;  // (whole half warps; no barrier below)
+  const int e = (int)(unit - row * 16 * kb) * 8;
+  const int n = max(0, min(8, C - e));
+  float v[8];
+  load8(X + row * C + e, n, vec, v);
+  const uint32_t mask = 0xffffu << (threadIdx.x & 16);
+  float m = amax8(v);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(mask, m, o));
+  const float inv = fp8_inverse(m);
+  if (n > 0) {
+    uint2 c;
+    c.x = fp8_pack4(v[0], v[1], v[2], v[3], inv);
+    c.y = fp8_pack4(v[4], v[5], v[6], v[7], inv);
+    *reinterpret_cast<uint2*>(Q + row * ldq + e) = c;
+  }
+  if ((threadIdx.x & 15) == 0) S[row * kb + e / 128] = fp8_scale(m);
+}
+
+// TILE: one scale a tile, else one for each 128 along the output's rows.
+// (TR = false is only used with TILE.)
+template <typename XT, bool TILE, bool TR>
+__global__ void __launch_bounds__(256)
+fp8_tile_kernel(const XT* __restrict__ X, uint8_t* __restrict__ Q, float* __restrict__ S,
+                int64_t R, int64_t C, int64_t ldq, int64_t rblocks, int64_t cblocks, int vec) {
+  __shared__ float top[16][128];
+  const int rr = threadIdx.x >> 4, cv = threadIdx.x & 15;
+  const int64_t rb = blockIdx.x / cblocks, cb = blockIdx.x - rb * cblocks;
+  const int64_t r0 = rb * 128 + rr * 8, c0 = cb * 128 + cv * 8;
+  const int nc = (int)max((int64_t)0, min((int64_t)8, C - c0));
+  float v[8][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const bool in = r0 + i < R;
+    load8(X + (in ? (r0 + i) * C + c0 : 0), in ? nc : 0, vec, v[i]);
+  }
+  float inv[8];
+  if constexpr (TILE) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max_nan(m, amax8(v[i]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if ((threadIdx.x & 31) == 0) top[0][threadIdx.x >> 5] = m;
+    __syncthreads();
+    m = top[0][0];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) m = max_nan(m, top[0][w]);
+    if (threadIdx.x == 0) S[TR ? cb * rblocks + rb : rb * cblocks + cb] = fp8_scale(m);
+    const float all = fp8_inverse(m);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) inv[e] = all;
+  } else {
+    // the largest of each column over the tile's 128 rows
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float m = fabsf(v[0][e]);
+#pragma unroll
+      for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(v[i][e]));
+      top[rr][cv * 8 + e] = m;
+    }
+    __syncthreads();
+    if (threadIdx.x < 128) {
+      float m = top[0][threadIdx.x];
+#pragma unroll
+      for (int k = 1; k < 16; ++k) m = max_nan(m, top[k][threadIdx.x]);
+      const int64_t c = cb * 128 + threadIdx.x;
+      if (c < C) S[c * rblocks + rb] = fp8_scale(m);
+      top[0][threadIdx.x] = fp8_inverse(m);  // (this thread alone uses the column)
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) inv[e] = top[0][cv * 8 + e];
+  }
+  if constexpr (!TR) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (r0 + i < R && nc > 0) {
+        uint2 c;
+        c.x = fp8_pack4(v[i][0], v[i][1], v[i][2], v[i][3], inv[0]);
+        c.y = fp8_pack4(v[i][4], v[i][5], v[i][6], v[i][7], inv[0]);
+        *reinterpret_cast<uint2*>(Q + (r0 + i) * ldq + c0) = c;
+      }
+    }
+  } else {
+    __shared__ uint2 turned[128][16];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      uint2 c;
+      c.x = fp8_pack4(v[0][e], v[1][e], v[2][e], v[3][e], inv[e]);
+      c.y = fp8_pack4(v[4][e], v[5][e], v[6][e], v[7][e], inv[e]);
+      turned[cv * 8 + e][rr ^ cv] = c;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int unit = k * 256 + threadIdx.x;
+      const int c = unit >> 3, part = (unit & 7) * 2, x = c >> 3;
+      const int64_t oc = cb * 128 + c, orow = rb * 128 + part * 8;
+      // (a row of Q has room for whole 16-byte pieces)
+      if (oc < C && orow < R) {
+        const uint2 a = turned[c][part ^ x], b = turned[c][(part + 1) ^ x];
+        *reinterpret_cast<uint4*>(Q + oc * ldq + orow) = make_uint4(a.x, a.y, b.x, b.y);
+      }
+    }
+  }
+}
+
+template <typename XT>
+kdn_status quantize_types(const void* x, void* q, float* scale, int64_t R, int64_t C, int64_t ldq,
+                          bool tile, bool tr, cudaStream_t s) {
+  const XT* X = static_cast<const XT*>(x);
+  uint8_t* Q = static_cast<uint8_t*>(q);
+  const int64_t rb = (R + 127) / 128, cb = (C + 127) / 128;
+  const int vec = C % 8 == 0;
+  if (!tile && !tr)
+    fp8_rows_kernel<XT><<<(unsigned)((R * cb * 16 + 255) / 256), 256, 0, s>>>(
+        X, Q, scale, R, (int)C, ldq, (int)cb, vec);
+  else if (tile && !tr)
+    fp8_tile_kernel<XT, true, false><<<(unsigned)(rb * cb), 256, 0, s>>>(X, Q, scale, R, C, ldq,
+                                                                         rb, cb, vec);
+  else if (tile)
+    fp8_tile_kernel<XT, true, true><<<(unsigned)(rb * cb), 256, 0, s>>>(X, Q, scale, R, C, ldq, rb,
+                                                                        cb, vec);
+  else
+    fp8_tile_kernel<XT, false, true><<<(unsigned)(rb * cb), 256, 0, s>>>(X, Q, scale, R, C, ldq,
+                                                                         rb, cb, vec);
+  return cudaGetLastError() == cudaSuccess ? KDN_OK : KDN_ERR_CUDA;
+}
+
+}  // namespace
+
+kdn_status fp8_quantize_launch(const void* x, kdn_dtype xt, void* q, int64_t ldq, float* scale,
+                               int64_t rows, int64_t cols, bool tile, bool transpose,
+                               cudaStream_t s) {
+  return xt == KDN_F32 ? quantize_types<float>(x, q, scale, rows, cols, ldq, tile, transpose, s)
+                       : quantize_types<__nv_bfloat16>(x, q, scale, rows, cols, ldq, tile,
+                                                       transpose, s);
+}
+
+}  // namespace kdn

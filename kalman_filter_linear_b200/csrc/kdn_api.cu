@@ -61,6 +61,34 @@ kdn_status kla_launch(kdn_dtype dt, const void* q, const void* k, const void* v,
                       const float* w, const float* r, const float* S0, const float* L0, float* o,
                       float* S_out, float* L_out, int B, int T, int H, int dk, int dv,
                       cudaStream_t s);
+size_t linear_scan_workspace_size(int B, int T, int D);
+kdn_status linear_scan_forward_launch(const void* a, const void* b, kdn_dtype gate_dtype,
+                                      const void* x, kdn_dtype in_dtype, const float* h0, void* y,
+                                      float* h_out, const int32_t* cu, int N, int B, int T, int D,
+                                      void* workspace, cudaStream_t s);
+kdn_status linear_scan_step_launch(const void* a, const void* b, kdn_dtype gate_dtype,
+                                   const void* x, kdn_dtype in_dtype, float* h, void* y, int64_t n,
+                                   cudaStream_t s);
+kdn_status linear_scan_backward_launch(const void* a, const void* b, kdn_dtype gate_dtype,
+                                       const void* x, const void* y, const void* dy,
+                                       kdn_dtype in_dtype, const float* h0, const float* dhT,
+                                       void* da, void* db, void* dx, float* dh0, const int32_t* cu,
+                                       int N, int B, int T, int D, void* workspace,
+                                       cudaStream_t s);
+kdn_status rmsnorm_forward_launch(const void* x, kdn_dtype xt, const void* res, kdn_dtype rt,
+                                  const float* w, void* h, void* y, kdn_dtype yt, int64_t ldy,
+                                  float* scale, int64_t rows, int D, float eps, cudaStream_t s);
+size_t rmsnorm_backward_workspace_size(int64_t rows, int D);
+kdn_status rmsnorm_backward_launch(const void* h, kdn_dtype ht, const float* w, const void* dy,
+                                   kdn_dtype yt, const void* dh, void* dx, kdn_dtype xt,
+                                   void* dres, float* dw, int64_t rows, int D, float eps,
+                                   void* workspace, cudaStream_t s);
+kdn_status fp8_quantize_launch(const void* x, kdn_dtype xt, void* q, int64_t ldq, float* scale,
+                               int64_t rows, int64_t cols, bool tile, bool transpose,
+                               cudaStream_t s);
+kdn_status fp8_matmul_launch(const void* x, int64_t ldx, const float* sx, const void* w,
+                             int64_t ldw, const float* sw, bool tile, void* out, kdn_dtype ot,
+                             int M, int N, int K, uint32_t* status, cudaStream_t s);
 }  // namespace kdn
 
 namespace {
@@ -214,7 +242,7 @@ const char* kdn_status_string(kdn_status status) {
   return "unknown kdn_status";
 }
 
-int kdn_version(void) { return 200; }
+int kdn_version(void) { return 300; }
 
 size_t kdn_mobius_scan_workspace_size(int64_t N, int64_t T) {
   return kdn::mobius_scan_workspace_size(N, T);
@@ -545,6 +573,184 @@ kdn_status kdn_forward_host(kdn_variant variant, const void* q, const void* k, c
         cudaStreamWaitEvent(s0, hs.done[j], 0) != cudaSuccess)
       status = KDN_ERR_CUDA;
   return status;
+}
+
+namespace {
+inline bool f32_or_bf16(kdn_dtype t) { return t == KDN_F32 || t == KDN_BF16; }
+inline size_t esize(kdn_dtype t) { return t == KDN_F32 ? 4 : t == KDN_BF16 ? 2 : 1; }
+constexpr int kScanMaxSteps = 1 << 30;
+constexpr int64_t kMaxElements = int64_t(1) << 40;
+
+// Shape of a linear scan: B entries of T steps (cu: N sequences in T steps).
+kdn_status scan_shape(const int32_t* cu, int B, int T, int D) {
+  if (B < 1 || T < 0 || D < 1 || T > kScanMaxSteps) return KDN_ERR_INVALID_ARG;
+  const int64_t entries = cu ? 1 : B;
+  if ((int64_t)B * D > kMaxElements || entries * std::max(T, 1) > kMaxElements / D)
+    return KDN_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(cu) & 3u) != 0) return KDN_ERR_INVALID_ARG;
+  // (the launch grid: a tile covers 64 channels and at least 64 steps)
+  const int64_t tiles = entries * ((D + 63) / 64) * std::max<int64_t>(1, (T + 63ll) / 64);
+  if (tiles > 0x7fffffffll) return KDN_ERR_UNSUPPORTED;
+  return KDN_OK;
+}
+kdn_status scan_workspace(const void* ws, size_t bytes, int B, int T, int D) {
+  if (!ws || bytes < kdn::linear_scan_workspace_size(B, T, D)) return KDN_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(ws) & 255u) return KDN_ERR_INVALID_ARG;
+  return KDN_OK;
+}
+}  // namespace
+
+size_t kdn_linear_scan_workspace_size(int B, int T, int D) {
+  if (scan_shape(nullptr, B, T, D) != KDN_OK) return 0;
+  return kdn::linear_scan_workspace_size(B, T, D);
+}
+
+kdn_status kdn_linear_scan_forward(const void* a, const void* b, kdn_dtype gate_dtype,
+                                   const void* x, kdn_dtype in_dtype, const float* h0,
+                                   const int32_t* cu_seqlens, void* y, float* h_out, int B, int T,
+                                   int D, void* workspace, size_t workspace_bytes, void* stream) {
+  // (without steps the [B, T, D] arrays are empty, and may be NULL)
+  if (!h_out || (T > 0 && (!a || !x || !y))) return KDN_ERR_INVALID_ARG;
+  if (!f32_or_bf16(gate_dtype) || !f32_or_bf16(in_dtype)) return KDN_ERR_INVALID_ARG;
+  if (!al16_or_null(a) || !al16_or_null(b) || !al16_or_null(x) || !al16_or_null(h0) ||
+      !al16_or_null(y) || !al16(h_out))
+    return KDN_ERR_INVALID_ARG;
+  kdn_status st = scan_shape(cu_seqlens, B, T, D);
+  if (st != KDN_OK) return st;
+  const int entries = cu_seqlens ? 1 : B;
+  st = scan_workspace(workspace, workspace_bytes, entries, T, D);
+  if (st != KDN_OK) return st;
+  return kdn::linear_scan_forward_launch(a, b, gate_dtype, x, in_dtype, h0, y, h_out, cu_seqlens,
+                                         B, entries, T, D, workspace, as_stream(stream));
+}
+
+kdn_status kdn_linear_scan_backward(const void* a, const void* b, kdn_dtype gate_dtype,
+                                    const void* x, const void* y, const void* dy,
+                                    kdn_dtype in_dtype, const float* h0, const float* dh_T,
+                                    const int32_t* cu_seqlens, void* da, void* db, void* dx,
+                                    float* dh0, int B, int T, int D, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+  if (!dh0 || (T > 0 && (!a || !y || !dy || !da || !dx))) return KDN_ERR_INVALID_ARG;
+  if (T > 0 && b && (!x || !db)) return KDN_ERR_INVALID_ARG;
+  if (!f32_or_bf16(gate_dtype) || !f32_or_bf16(in_dtype)) return KDN_ERR_INVALID_ARG;
+  if (!al16_or_null(a) || !al16_or_null(b) || !al16_or_null(x) || !al16_or_null(y) ||
+      !al16_or_null(dy) || !al16_or_null(h0) || !al16_or_null(dh_T) || !al16_or_null(da) ||
+      !al16_or_null(db) || !al16_or_null(dx) || !al16(dh0))
+    return KDN_ERR_INVALID_ARG;
+  kdn_status st = scan_shape(cu_seqlens, B, T, D);
+  if (st != KDN_OK) return st;
+  const int entries = cu_seqlens ? 1 : B;
+  st = scan_workspace(workspace, workspace_bytes, entries, T, D);
+  if (st != KDN_OK) return st;
+  return kdn::linear_scan_backward_launch(a, b, gate_dtype, x, y, dy, in_dtype, h0, dh_T, da, db,
+                                          dx, dh0, cu_seqlens, B, entries, T, D, workspace,
+                                          as_stream(stream));
+}
+
+kdn_status kdn_linear_scan_step(const void* a, const void* b, kdn_dtype gate_dtype, const void* x,
+                                kdn_dtype in_dtype, float* h, void* y, int B, int D,
+                                void* stream) {
+  if (!a || !x || !h || !y) return KDN_ERR_INVALID_ARG;
+  if (!f32_or_bf16(gate_dtype) || !f32_or_bf16(in_dtype)) return KDN_ERR_INVALID_ARG;
+  if (!al16(a) || !al16_or_null(b) || !al16(x) || !al16(h) || !al16(y)) return KDN_ERR_INVALID_ARG;
+  if (B < 1 || D < 1 || (int64_t)B * D > kMaxElements) return KDN_ERR_INVALID_ARG;
+  return kdn::linear_scan_step_launch(a, b, gate_dtype, x, in_dtype, h, y, (int64_t)B * D,
+                                      as_stream(stream));
+}
+
+namespace {
+constexpr int kNormMaxDim = 16384;
+inline bool norm_shape(int64_t rows, int D, float eps) {
+  return rows >= 0 && rows <= 0x7fffffffll && D >= 1 && eps >= 0.f && eps <= 3.0e38f;
+}
+// an 8-bit matrix: rows on 16-byte boundaries, ld at least the row's length
+inline bool fp8_matrix(const void* q, int64_t ld, int64_t cols) {
+  return q && al16(q) && ld >= cols && ld % 16 == 0 && ld < (int64_t(1) << 36);
+}
+}  // namespace
+
+kdn_status kdn_rmsnorm_forward(const void* x, kdn_dtype x_dtype, const void* residual,
+                               kdn_dtype residual_dtype, const float* weight, void* h, void* y,
+                               kdn_dtype y_dtype, int64_t ldy, float* scale, int64_t rows, int D,
+                               float eps, void* stream) {
+  if (!x || !weight || !y) return KDN_ERR_INVALID_ARG;
+  if (!f32_or_bf16(x_dtype)) return KDN_ERR_INVALID_ARG;
+  if (!f32_or_bf16(y_dtype) && y_dtype != KDN_E4M3) return KDN_ERR_INVALID_ARG;
+  if (residual ? !f32_or_bf16(residual_dtype) || !h : h != nullptr) return KDN_ERR_INVALID_ARG;
+  if (!al16(x) || !al16_or_null(residual) || !al16(weight) || !al16_or_null(h) || !al16(y))
+    return KDN_ERR_INVALID_ARG;
+  if (!norm_shape(rows, D, eps)) return KDN_ERR_INVALID_ARG;
+  if (y_dtype == KDN_E4M3) {
+    if (!scale || (reinterpret_cast<uintptr_t>(scale) & 3u) || !fp8_matrix(y, ldy, D))
+      return KDN_ERR_INVALID_ARG;
+  }
+  if (D > kNormMaxDim) return KDN_ERR_UNSUPPORTED;
+  if (rows == 0) return KDN_OK;
+  return kdn::rmsnorm_forward_launch(x, x_dtype, residual, residual_dtype, weight, h, y, y_dtype,
+                                     ldy, scale, rows, D, eps, as_stream(stream));
+}
+
+size_t kdn_rmsnorm_backward_workspace_size(int64_t rows, int D) {
+  if (!norm_shape(rows, D, 0.f) || D > kNormMaxDim) return 0;
+  return kdn::rmsnorm_backward_workspace_size(rows, D);
+}
+
+kdn_status kdn_rmsnorm_backward(const void* h, kdn_dtype h_dtype, const float* weight,
+                                const void* dy, kdn_dtype dy_dtype, const void* dh, void* dx,
+                                kdn_dtype dx_dtype, void* dresidual, float* dweight, int64_t rows,
+                                int D, float eps, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+  if (!h || !weight || !dy || !dx || !dweight) return KDN_ERR_INVALID_ARG;
+  if (!f32_or_bf16(h_dtype) || !f32_or_bf16(dy_dtype) || !f32_or_bf16(dx_dtype))
+    return KDN_ERR_INVALID_ARG;
+  if (!al16(h) || !al16(weight) || !al16(dy) || !al16_or_null(dh) || !al16(dx) ||
+      !al16_or_null(dresidual) || !al16(dweight))
+    return KDN_ERR_INVALID_ARG;
+  if (!norm_shape(rows, D, eps)) return KDN_ERR_INVALID_ARG;
+  if (D > kNormMaxDim) return KDN_ERR_UNSUPPORTED;
+  const size_t need = kdn::rmsnorm_backward_workspace_size(rows, D);
+  if (need && (!workspace || workspace_bytes < need)) return KDN_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return KDN_ERR_INVALID_ARG;
+  return kdn::rmsnorm_backward_launch(h, h_dtype, weight, dy, dy_dtype, dh, dx, dx_dtype,
+                                      dresidual, dweight, rows, D, eps, workspace,
+                                      as_stream(stream));
+}
+
+kdn_status kdn_fp8_quantize(const void* x, kdn_dtype x_dtype, int64_t rows, int64_t cols, int tile,
+                            int transpose, void* q, int64_t ldq, float* scale, void* stream) {
+  if (!x || !q || !scale) return KDN_ERR_INVALID_ARG;
+  if (!f32_or_bf16(x_dtype) || rows < 0 || cols < 1) return KDN_ERR_INVALID_ARG;
+  if (rows > 0x7fffffffll || cols > 0x7fffffffll || rows > kMaxElements / cols)
+    return KDN_ERR_INVALID_ARG;
+  if (!al16(x) || (reinterpret_cast<uintptr_t>(scale) & 3u) ||
+      !fp8_matrix(q, ldq, transpose ? rows : cols))
+    return KDN_ERR_INVALID_ARG;
+  const int64_t kb = (cols + 127) / 128;
+  // (the launch grid)
+  if (((rows + 127) / 128) * kb > 0x7fffffffll || (rows * kb * 16 + 255) / 256 > 0x7fffffffll)
+    return KDN_ERR_UNSUPPORTED;
+  if (rows == 0) return KDN_OK;
+  return kdn::fp8_quantize_launch(x, x_dtype, q, ldq, scale, rows, cols, tile != 0, transpose != 0,
+                                  as_stream(stream));
+}
+
+kdn_status kdn_fp8_matmul(const void* x, int64_t ldx, const float* x_scale, const void* w,
+                          int64_t ldw, const float* w_scale, int w_tile, void* out,
+                          kdn_dtype out_dtype, int M, int N, int K, uint32_t* status,
+                          void* stream) {
+  if (!x || !x_scale || !w || !w_scale || !out) return KDN_ERR_INVALID_ARG;
+  if (!f32_or_bf16(out_dtype) || M < 0 || N < 1 || K < 1) return KDN_ERR_INVALID_ARG;
+  if (!fp8_matrix(x, ldx, K) || !fp8_matrix(w, ldw, K) || !al16(out)) return KDN_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(x_scale) & 3u) || (reinterpret_cast<uintptr_t>(w_scale) & 3u) ||
+      (reinterpret_cast<uintptr_t>(status) & 3u))
+    return KDN_ERR_INVALID_ARG;
+  // (tile counts and coordinates are 32-bit)
+  if (M > 0x7fffff00 || N > 0x7fffff00 || K > 0x7fffff00 ||
+      ((int64_t)M + 15) / 16 * (((int64_t)N + 127) / 128) * 8 > 0x7fffffffll)
+    return KDN_ERR_UNSUPPORTED;
+  if (M == 0) return KDN_OK;
+  return kdn::fp8_matmul_launch(x, ldx, x_scale, w, ldw, w_scale, w_tile != 0, out, out_dtype, M,
+                                N, K, status, as_stream(stream));
 }
 
 kdn_status kdn_read_workspace_status(const void* workspace, size_t workspace_bytes,

@@ -19,7 +19,7 @@ LIB_PATH = os.path.join(_PKG, 'libkdn.so')
 
 KDN_OK, KDN_ERR_INVALID_ARG, KDN_ERR_UNSUPPORTED, KDN_ERR_WORKSPACE, KDN_ERR_TIMEOUT, \
     KDN_ERR_CUDA = range(6)
-KDN_F32, KDN_BF16 = 0, 1
+KDN_F32, KDN_BF16, KDN_E4M3 = 0, 1, 2
 KDN_ISO, KDN_DIAG = 0, 1
 KDN_CHUNK_AUTO, KDN_CHUNK_RECURRENT, KDN_CHUNK_64 = 0, 1, 64
 
@@ -87,6 +87,29 @@ def lib():
     L.kdn_kla_forward_ws.restype = _i32
     L.kdn_kla_forward_ws.argtypes = [_vp, _vp, _vp, _i32] + [_vp] * 8 + [_i32] * 5 + \
         [_vp, _sz, _vp]
+    L.kdn_linear_scan_workspace_size.restype = _sz
+    L.kdn_linear_scan_workspace_size.argtypes = [_i32] * 3
+    L.kdn_linear_scan_forward.restype = _i32
+    L.kdn_linear_scan_forward.argtypes = [_vp, _vp, _i32, _vp, _i32] + [_vp] * 4 + [_i32] * 3 + \
+        [_vp, _sz, _vp]
+    L.kdn_linear_scan_backward.restype = _i32
+    L.kdn_linear_scan_backward.argtypes = [_vp, _vp, _i32, _vp, _vp, _vp, _i32] + [_vp] * 7 + \
+        [_i32] * 3 + [_vp, _sz, _vp]
+    L.kdn_linear_scan_step.restype = _i32
+    L.kdn_linear_scan_step.argtypes = [_vp, _vp, _i32, _vp, _i32, _vp, _vp, _i32, _i32, _vp]
+    L.kdn_rmsnorm_forward.restype = _i32
+    L.kdn_rmsnorm_forward.argtypes = [_vp, _i32, _vp, _i32, _vp, _vp, _vp, _i32, _i64, _vp, _i64,
+                                      _i32, _f32, _vp]
+    L.kdn_rmsnorm_backward_workspace_size.restype = _sz
+    L.kdn_rmsnorm_backward_workspace_size.argtypes = [_i64, _i32]
+    L.kdn_rmsnorm_backward.restype = _i32
+    L.kdn_rmsnorm_backward.argtypes = [_vp, _i32, _vp, _vp, _i32, _vp, _vp, _i32, _vp, _vp, _i64,
+                                       _i32, _f32, _vp, _sz, _vp]
+    L.kdn_fp8_quantize.restype = _i32
+    L.kdn_fp8_quantize.argtypes = [_vp, _i32, _i64, _i64, _i32, _i32, _vp, _i64, _vp, _vp]
+    L.kdn_fp8_matmul.restype = _i32
+    L.kdn_fp8_matmul.argtypes = [_vp, _i64, _vp, _vp, _i64, _vp, _i32, _vp, _i32, _i32, _i32,
+                                 _i32, _vp, _vp]
     L.kdn_read_workspace_status.restype = _i32
     L.kdn_read_workspace_status.argtypes = [_vp, _sz, _vp]
     L.kdn_testing_mobius_scan_unpublished_tile.restype = _i32
@@ -514,6 +537,320 @@ def kdn_kla_forward(q, k, v, a, w, r, S0=None, lam0=None, o=None, S_out=None, la
                                   workspace.numel(), _stream())
     _check(st, 'kdn_kla_forward_ws')
     return o, S_out, lam_out
+
+
+# ------------------------------------------ linear recurrence, norm, 8 bits
+# These calls run on the device of their tensors (which may differ from the
+# current one) and on that device's current stream.
+
+_CODE = {torch.float32: KDN_F32, torch.bfloat16: KDN_BF16, torch.float8_e4m3fn: KDN_E4M3}
+
+
+def _float_code(t, name):
+    if t.dtype != torch.float32 and t.dtype != torch.bfloat16:
+        raise TypeError(f'{name} must be bfloat16 or float32, got {t.dtype}')
+    return _CODE[t.dtype]
+
+
+def _arg(t, name, dtype, shape, dev):
+    """The data pointer of a checked tensor (None for a missing one)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f'{name} must be a CUDA tensor')
+    if t.dtype != dtype:
+        raise TypeError(f'{name} must be {dtype}, got {t.dtype}')
+    if t.shape != shape:
+        raise ValueError(f'{name} must have shape {tuple(shape)}, got {tuple(t.shape)}')
+    if not t.is_contiguous():
+        raise ValueError(f'{name} must be contiguous')
+    if t.device != dev:
+        raise ValueError(f'{name} must be on {dev}, got {t.device}')
+    return t.data_ptr()
+
+
+def _cuda_tensor(t, name, ndim):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f'{name} must be a CUDA tensor')
+    if t.dim() not in ndim:
+        raise ValueError(f'{name} must have {" or ".join(map(str, ndim))} dimensions, '
+                         f'got {t.dim()}')
+    return t.device
+
+
+def _call(fn, dev, *args):
+    """Call an entry point with `dev` current, on its current stream."""
+    if torch.cuda.current_device() == dev.index:
+        return fn(*args, torch.cuda.current_stream().cuda_stream)
+    with torch.cuda.device(dev):
+        return fn(*args, torch.cuda.current_stream().cuda_stream)
+
+
+def _ws_arg(workspace, need, dev):
+    """(tensor, pointer, bytes) of a workspace of at least `need` bytes."""
+    if workspace is None:
+        if need == 0:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif not isinstance(workspace, torch.Tensor) or workspace.device != dev or \
+            not workspace.is_contiguous():
+        raise TypeError(f'workspace must be a contiguous CUDA tensor on {dev}')
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def kdn_linear_scan_workspace_size(B, T, D):
+    return int(lib().kdn_linear_scan_workspace_size(B, T, D))
+
+
+def _scan_dims(a, cu_seqlens):
+    dev = _cuda_tensor(a, 'a', (3,) if cu_seqlens is None else (2,))
+    if cu_seqlens is None:
+        B, T, D = a.shape
+        return dev, B, T, D, kdn_linear_scan_workspace_size(B, T, D)
+    T, D = a.shape
+    if not isinstance(cu_seqlens, torch.Tensor) or not cu_seqlens.is_cuda:
+        raise TypeError('cu_seqlens must be a CUDA tensor')
+    return dev, cu_seqlens.numel() - 1, T, D, kdn_linear_scan_workspace_size(1, T, D)
+
+
+def kdn_linear_scan_forward(a, x, b=None, h0=None, cu_seqlens=None, y=None, h_out=None,
+                            workspace=None):
+    """The gated linear recurrence h_t = a_t h_{t-1} + b_t x_t: a, b, x
+    [B, T, D], or [T, D] with cu_seqlens [B + 1] int32 (packed sequences);
+    a and b share a dtype (fp32 or bf16), h0 [B, D] fp32.  Returns (y like x,
+    h_T [B, D] fp32).  With cu_seqlens, the rows of y behind the last sequence
+    are left as they were."""
+    dev, B, T, D, need = _scan_dims(a, cu_seqlens)
+    f, shape, ends = torch.float32, a.shape, (B, D)
+    gate = _float_code(a, 'a')
+    xt = _float_code(x, 'x')
+    pa, pb, px = a.data_ptr(), _arg(b, 'b', a.dtype, shape, dev), _arg(x, 'x', x.dtype, shape, dev)
+    if not a.is_contiguous():
+        raise ValueError('a must be contiguous')
+    p0 = _arg(h0, 'h0', f, ends, dev)
+    pc = _arg(cu_seqlens, 'cu_seqlens', torch.int32, (B + 1,), dev)
+    if y is None:
+        y = torch.empty_like(x)
+    if h_out is None:
+        h_out = torch.empty(ends, dtype=f, device=dev)
+    workspace, pw, nw = _ws_arg(workspace, need, dev)
+    st = _call(lib().kdn_linear_scan_forward, dev, pa, pb, gate, px, xt, p0, pc,
+               _arg(y, 'y', x.dtype, shape, dev), _arg(h_out, 'h_out', f, ends, dev), B, T, D, pw,
+               nw)
+    _check(st, 'kdn_linear_scan_forward')
+    return y, h_out
+
+
+def kdn_linear_scan_backward(a, x, y, dy, b=None, h0=None, dh_T=None, cu_seqlens=None, da=None,
+                             dx=None, db=None, dh0=None, workspace=None):
+    """The gradients of kdn_linear_scan_forward, given its output y, dy like y
+    and dh_T [B, D] fp32 (or None): a dict of a, x, h0 (fp32) and, when b is
+    given, b.  x is read only with b, and may be None without."""
+    dev, B, T, D, need = _scan_dims(a, cu_seqlens)
+    f, shape, ends = torch.float32, a.shape, (B, D)
+    gate = _float_code(a, 'a')
+    yt = _float_code(y, 'y')
+    if b is not None and x is None:
+        raise ValueError('x is needed for the gradient of b')
+    if not a.is_contiguous():
+        raise ValueError('a must be contiguous')
+    pa, pb = a.data_ptr(), _arg(b, 'b', a.dtype, shape, dev)
+    px, py = _arg(x, 'x', y.dtype, shape, dev), _arg(y, 'y', y.dtype, shape, dev)
+    pdy = _arg(dy, 'dy', y.dtype, shape, dev)
+    p0, pT = _arg(h0, 'h0', f, ends, dev), _arg(dh_T, 'dh_T', f, ends, dev)
+    pc = _arg(cu_seqlens, 'cu_seqlens', torch.int32, (B + 1,), dev)
+    da = torch.empty_like(a) if da is None else da
+    dx = torch.empty_like(y) if dx is None else dx
+    if b is not None and db is None:
+        db = torch.empty_like(b)
+    dh0 = torch.empty(ends, dtype=f, device=dev) if dh0 is None else dh0
+    workspace, pw, nw = _ws_arg(workspace, need, dev)
+    st = _call(lib().kdn_linear_scan_backward, dev, pa, pb, gate, px, py, pdy, yt, p0, pT, pc,
+               _arg(da, 'da', a.dtype, shape, dev),
+               _arg(db, 'db', a.dtype, shape, dev) if b is not None else None,
+               _arg(dx, 'dx', y.dtype, shape, dev), _arg(dh0, 'dh0', f, ends, dev), B, T, D, pw,
+               nw)
+    _check(st, 'kdn_linear_scan_backward')
+    g = dict(a=da, x=dx, h0=dh0)
+    if b is not None:
+        g['b'] = db
+    return g
+
+
+def kdn_linear_scan_step(a, x, h, b=None, y=None):
+    """One step of the recurrence: a, b, x [B, D], h [B, D] fp32 updated in
+    place.  Returns y like x."""
+    dev = _cuda_tensor(a, 'a', (2,))
+    shape = a.shape
+    gate, xt = _float_code(a, 'a'), _float_code(x, 'x')
+    if y is None:
+        y = torch.empty_like(x)
+    st = _call(lib().kdn_linear_scan_step, dev, _arg(a, 'a', a.dtype, shape, dev),
+               _arg(b, 'b', a.dtype, shape, dev), gate, _arg(x, 'x', x.dtype, shape, dev), xt,
+               _arg(h, 'h', torch.float32, shape, dev), _arg(y, 'y', x.dtype, shape, dev),
+               shape[0], shape[1])
+    _check(st, 'kdn_linear_scan_step')
+    return y
+
+
+def _fp8_empty(rows, cols, dev):
+    """An e4m3 matrix whose rows start on 16-byte boundaries."""
+    ld = (cols + 15) // 16 * 16
+    q = torch.empty((rows, ld), dtype=torch.float8_e4m3fn, device=dev)
+    return q if ld == cols else q[:, :cols]
+
+
+def _fp8_arg(q, name, rows, cols, dev):
+    """(pointer, row distance in bytes) of an e4m3 matrix."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise TypeError(f'{name} must be a CUDA tensor')
+    if q.dtype != torch.float8_e4m3fn:
+        raise TypeError(f'{name} must be torch.float8_e4m3fn, got {q.dtype}')
+    if q.shape != (rows, cols):
+        raise ValueError(f'{name} must have shape {(rows, cols)}, got {tuple(q.shape)}')
+    if q.device != dev:
+        raise ValueError(f'{name} must be on {dev}, got {q.device}')
+    ld = q.stride(0) if rows > 1 else (cols + 15) // 16 * 16
+    if (cols > 1 and q.stride(1) != 1) or ld % 16 or ld < cols:
+        raise ValueError(f'the rows of {name} must be contiguous and a multiple of 16 bytes apart '
+                         f'(kdn_fp8_quantize lays them out so), got strides {q.stride()}')
+    return q.data_ptr(), ld
+
+
+def kdn_rmsnorm_forward(x, weight, residual=None, eps=1e-6, out_dtype=torch.bfloat16, y=None,
+                        scale=None, h=None):
+    """Residual addition and RMS norm over the last dimension: x [rows, D] or
+    [..., D], residual like x (its own dtype), weight [D] fp32.  Returns
+    (y, scale, h): y in out_dtype (bfloat16, float32 or float8_e4m3fn), scale
+    [rows, ceil(D / 128)] for e4m3 else None, and h = x + residual in the
+    residual's dtype (None without a residual).  An e4m3 y is two-dimensional,
+    its rows on 16-byte boundaries."""
+    dev = _cuda_tensor(x, 'x', range(1, 9))
+    D = x.shape[-1]
+    rows = x.numel() // D if D else 0
+    xt = _float_code(x, 'x')
+    if out_dtype not in _CODE:
+        raise TypeError(f'out_dtype must be bfloat16, float32 or float8_e4m3fn, got {out_dtype}')
+    px, pw = _arg(x, 'x', x.dtype, x.shape, dev), _arg(weight, 'weight', torch.float32, (D,), dev)
+    if pw is None:
+        raise TypeError('weight must be a CUDA tensor')
+    rt, pr, ph = KDN_F32, None, None
+    if residual is not None:
+        rt, pr = _float_code(residual, 'residual'), _arg(residual, 'residual', residual.dtype,
+                                                         x.shape, dev)
+        h = torch.empty_like(residual) if h is None else h
+        ph = _arg(h, 'h', residual.dtype, x.shape, dev)
+    elif h is not None:
+        raise ValueError('h is an output only with a residual')
+    ld, ps = 0, None
+    if out_dtype == torch.float8_e4m3fn:
+        y = _fp8_empty(rows, D, dev) if y is None else y
+        py, ld = _fp8_arg(y, 'y', rows, D, dev)
+        blocks = (rows, (D + 127) // 128)
+        scale = torch.empty(blocks, dtype=torch.float32, device=dev) if scale is None else scale
+        ps = _arg(scale, 'scale', torch.float32, blocks, dev)
+    else:
+        if scale is not None:
+            raise ValueError('scale is an output only for float8_e4m3fn')
+        y = torch.empty(x.shape, dtype=out_dtype, device=dev) if y is None else y
+        py = _arg(y, 'y', out_dtype, x.shape, dev)
+    if rows:
+        st = _call(lib().kdn_rmsnorm_forward, dev, px, xt, pr, rt, pw, ph, py, _CODE[out_dtype],
+                   ld, ps, rows, D, eps)
+        _check(st, 'kdn_rmsnorm_forward')
+    return y, scale, h
+
+
+def kdn_rmsnorm_backward_workspace_size(rows, D):
+    return int(lib().kdn_rmsnorm_backward_workspace_size(rows, D))
+
+
+def kdn_rmsnorm_backward(h, weight, dy, dh=None, eps=1e-6, x_dtype=None, want_residual=None,
+                         dx=None, dresidual=None, dweight=None, workspace=None):
+    """The gradients of kdn_rmsnorm_forward: h its h (x without a residual),
+    dy like h in bfloat16 or float32, dh the gradient that reaches h from its
+    other use (h's dtype, or None).  Returns a dict of x (in x_dtype, h's by
+    default), weight (fp32) and residual (h's dtype; by default when dh is
+    given, else None)."""
+    dev = _cuda_tensor(h, 'h', range(1, 9))
+    D = h.shape[-1]
+    rows = h.numel() // D if D else 0
+    x_dtype = h.dtype if x_dtype is None else x_dtype
+    ht, yt = _float_code(h, 'h'), _float_code(dy, 'dy')
+    if x_dtype != torch.float32 and x_dtype != torch.bfloat16:
+        raise TypeError(f'x_dtype must be bfloat16 or float32, got {x_dtype}')
+    if want_residual is None:
+        want_residual = dh is not None or dresidual is not None
+    f, shape = torch.float32, h.shape
+    ph, pw = _arg(h, 'h', h.dtype, shape, dev), _arg(weight, 'weight', f, (D,), dev)
+    pdy, pdh = _arg(dy, 'dy', dy.dtype, shape, dev), _arg(dh, 'dh', h.dtype, shape, dev)
+    dx = torch.empty(shape, dtype=x_dtype, device=dev) if dx is None else dx
+    if want_residual and dresidual is None:
+        dresidual = torch.empty(shape, dtype=h.dtype, device=dev)
+    dweight = torch.empty(D, dtype=f, device=dev) if dweight is None else dweight
+    px, pr = _arg(dx, 'dx', x_dtype, shape, dev), _arg(dresidual, 'dresidual', h.dtype, shape, dev)
+    pdw = _arg(dweight, 'dweight', f, (D,), dev)
+    if rows == 0:
+        dweight.zero_()
+    else:
+        workspace, pws, nws = _ws_arg(workspace, kdn_rmsnorm_backward_workspace_size(rows, D), dev)
+        st = _call(lib().kdn_rmsnorm_backward, dev, ph, ht, pw, pdy, yt, pdh, px, _CODE[x_dtype],
+                   pr, pdw, rows, D, eps, pws, nws)
+        _check(st, 'kdn_rmsnorm_backward')
+    return dict(x=dx, weight=dweight, residual=dresidual)
+
+
+def kdn_fp8_quantize(x, tile=False, transpose=False, q=None, scale=None):
+    """x [rows, cols] (bfloat16 or float32) in e4m3 with fp32 scales: one for
+    each 128 of an output row, or with tile=True for each 128 x 128 tile;
+    transpose=True quantises x's transpose.  Returns (q [R, C], its rows on
+    16-byte boundaries; scale [R or ceil(R / 128), ceil(C / 128)])."""
+    dev = _cuda_tensor(x, 'x', (2,))
+    rows, cols = x.shape
+    xt = _float_code(x, 'x')
+    px = _arg(x, 'x', x.dtype, x.shape, dev)
+    R, C = (cols, rows) if transpose else (rows, cols)
+    blocks = ((R + 127) // 128 if tile else R, (C + 127) // 128)
+    q = _fp8_empty(R, C, dev) if q is None else q
+    scale = torch.empty(blocks, dtype=torch.float32, device=dev) if scale is None else scale
+    pq, ld = _fp8_arg(q, 'q', R, C, dev)
+    ps = _arg(scale, 'scale', torch.float32, blocks, dev)
+    if rows and cols:
+        st = _call(lib().kdn_fp8_quantize, dev, px, xt, rows, cols, int(tile), int(transpose), pq,
+                   ld, ps)
+        _check(st, 'kdn_fp8_quantize')
+    return q, scale
+
+
+def kdn_fp8_matmul(x, x_scale, w, w_scale, out_dtype=torch.bfloat16, out=None, status=None):
+    """The 8-bit projection x w^T: x [M, K] and w [N, K] in e4m3 (rows on
+    16-byte boundaries, as kdn_fp8_quantize lays them out), x_scale
+    [M, ceil(K / 128)], w_scale [ceil(N / 128), ceil(K / 128)] (128 x 128
+    tiles) or [N, ceil(K / 128)], fp32.  Returns [M, N] in out_dtype (bfloat16
+    or float32).  status: one zeroed int32 word that a timed-out wait sets."""
+    dev = _cuda_tensor(x, 'x', (2,))
+    _cuda_tensor(w, 'w', (2,))
+    M, K = x.shape
+    N = w.shape[0]
+    px, ldx = _fp8_arg(x, 'x', M, K, dev)
+    pw, ldw = _fp8_arg(w, 'w', N, K, dev)
+    kb = (K + 127) // 128
+    psx = _arg(x_scale, 'x_scale', torch.float32, (M, kb), dev)
+    _cuda_tensor(w_scale, 'w_scale', (2,))
+    tile = w_scale.shape[0] != N  # (the two forms agree for N = 1)
+    psw = _arg(w_scale, 'w_scale', torch.float32, ((N + 127) // 128 if tile else N, kb), dev)
+    if psx is None:
+        raise TypeError('x_scale must be a CUDA tensor')
+    if out_dtype != torch.float32 and out_dtype != torch.bfloat16:
+        raise TypeError(f'out_dtype must be bfloat16 or float32, got {out_dtype}')
+    out = torch.empty((M, N), dtype=out_dtype, device=dev) if out is None else out
+    po = _arg(out, 'out', out_dtype, (M, N), dev)
+    pst = _arg(status, 'status', torch.int32, (1,), dev)
+    if M:
+        st = _call(lib().kdn_fp8_matmul, dev, px, ldx, psx, pw, ldw, psw, int(tile), po,
+                   _CODE[out_dtype], M, N, K, pst)
+        _check(st, 'kdn_fp8_matmul')
+    return out
 
 
 def kdn_read_workspace_status(workspace):

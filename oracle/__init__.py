@@ -15,6 +15,9 @@ Modules:
   kla_ref       the information-form diagonal filter (KLA): Mobius precision
                 recursion, affine mean recursion, precision-ratio gates
   kdn_grad      the reverse-mode (adjoint) gradient of the KDN forward
+  linear_scan_ref  the gated linear recurrence and its adjoint
+  rmsnorm_ref   the residual RMS norm and its gradient
+  fp8_ref       the e4m3 block format and its product
 
 Sources (page titles as printed on the pages):
   [KDN-abs]  "Kalman Delta Networks: Uncertainty-aware Associative Memory",
@@ -29,7 +32,9 @@ Sources (page titles as printed on the pages):
 Parity pins: every function here is pinned against something other than
 itself -- ``tests/test_oracle_pins.py`` (brute-force Gaussian conditioning,
 numerical KL minimisation, closed forms, Mobius algebra, the gated delta rule,
-invariants), ``tests/test_kla_pins.py`` (scalar-chain conditioning, the
+invariants), ``tests/test_layer_pins.py`` (finite differences, closed forms and
+torch's own e4m3 for the recurrence, the norm and the 8-bit blocks),
+``tests/test_kla_pins.py`` (scalar-chain conditioning, the
 Diagonal KDN special cases, the precision fixed point) and
 ``tests/test_grad_pins.py`` (finite differences of the forward).  The one
 "parity unpinned" item is agreement with the KDN paper's own equations, which
