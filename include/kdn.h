@@ -466,7 +466,8 @@ kdn_status kdn_kla_forward_ws(const void* q, const void* k, const void* v,
  * state per channel; the steps compose by an associative scan, one pass over
  * the data.
  *
- * a        [B, T, D] gate_dtype device: any values (a forget gate is in [0, 1])
+ * a        [B, T, D] gate_dtype device: a forget gate is in [0, 1]; other values
+ *          do as long as products of up to 128 consecutive ones stay finite
  * b        [B, T, D] gate_dtype device, or NULL for ones
  * x        [B, T, D] in_dtype device
  * h0       [B, D] fp32 device initial states, or NULL for zeros

@@ -588,8 +588,8 @@ kdn_status scan_shape(const int32_t* cu, int B, int T, int D) {
   if ((int64_t)B * D > kMaxElements || entries * std::max(T, 1) > kMaxElements / D)
     return KDN_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(cu) & 3u) != 0) return KDN_ERR_INVALID_ARG;
-  // (the launch grid: a tile covers 64 channels and at least 64 steps)
-  const int64_t tiles = entries * ((D + 63) / 64) * std::max<int64_t>(1, (T + 63ll) / 64);
+  // (tiles are counted in 32 bits: one covers 64 channels and at least 32 steps)
+  const int64_t tiles = entries * ((D + 63) / 64) * std::max<int64_t>(1, (T + 31ll) / 32);
   if (tiles > 0x7fffffffll) return KDN_ERR_UNSUPPORTED;
   return KDN_OK;
 }

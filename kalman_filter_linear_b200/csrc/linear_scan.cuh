@@ -6,6 +6,11 @@
 // recurrence run from the last step to the first on other inputs, so both
 // directions share the tile, the look-back across tiles and this map.
 //
+// Most calls run in the streaming form (linear_scan_stream.cuh).  The form below
+// is for one or two columns of 64 channels over many steps, where its tiles
+// spread over the whole device, and for packed sequences whose states are
+// updated in place, since a tile here reads its inputs once.
+//
 // Tile: 8 warps, 64 channels, 8 * L steps.  Warp w takes the L consecutive
 // steps w L ... of the tile's order, lane l the channels 2 l and 2 l + 1, and
 // all inputs of a step range sit in registers: one read of every input, and a
@@ -32,8 +37,9 @@ namespace kdn {
 constexpr int kLsWarps = 8;
 constexpr int kLsThreads = kLsWarps * 32;
 constexpr int kLsChannels = 64;  // channels of a tile
-constexpr int kLsFwdSteps = 16;  // steps of a warp, forward
+constexpr int kLsFwdSteps = 8;   // steps of a warp, forward (16 spill)
 constexpr int kLsBwdSteps = 8;   // steps of a warp, backward
+constexpr int kLsShortestTile = 32;  // steps of the shortest tile of any kernel
 
 struct LsWs {
   uint32_t* error;    // device error word
@@ -146,8 +152,8 @@ __device__ __forceinline__ float2 ls_look_back(const LsWs& ws, int64_t j, int64_
                                                int64_t cols, bool last, float4 m, float2 init) {
   const int lane = threadIdx.x & 31;
   const int64_t tile = j * cols + col;
+  // (the warp barrier puts every lane's stores before lane 0's release)
   auto publish = [&](uint32_t what) {
-    __threadfence();
     __syncwarp();
     if (lane == 0) st_release_u32(ws.flag + tile, what);
   };
@@ -213,10 +219,9 @@ struct LsPlan {
   int64_t chunks, cols;  // step ranges, (batch entry, channel group) columns
   size_t flag, map, state, bytes;
 };
-inline LsPlan ls_plan(int64_t B, int64_t T, int64_t D, int steps) {
+inline LsPlan ls_plan(int64_t B, int64_t T, int64_t D, int64_t per /* steps of a tile */) {
   LsPlan p{};
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  const int64_t per = (int64_t)steps * kLsWarps;
   p.chunks = T > 0 ? (T + per - 1) / per : 1;
   p.cols = B * ((D + kLsChannels - 1) / kLsChannels);
   const size_t tiles = (size_t)(p.chunks * p.cols);

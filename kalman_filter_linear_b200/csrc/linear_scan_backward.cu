@@ -10,6 +10,7 @@
 // rounded value (half a bf16 step of relative error in da, as da's own
 // rounding), which saves running the forward again.
 #include "linear_scan.cuh"
+#include "linear_scan_call.h"
 
 namespace kdn {
 namespace {
@@ -164,32 +165,28 @@ linear_scan_backward_kernel(const GT* __restrict__ Ag, const GT* __restrict__ Bg
   }
 }
 
-struct Args {
-  const void *a, *b, *x, *y, *dy;
-  const float *h0, *dhT;
-  void *da, *db, *dx;
-  float* dh0;
-  const int32_t* cu;
-  int N, B, T, D;
-};
-
 template <typename GT, typename XT, bool HAS_B, bool PACKED, bool EVEN>
-kdn_status backward_launch_t(const Args& k, const LsPlan& p, const LsWs& ws, cudaStream_t s) {
+kdn_status backward_go(const LsCall& k) {
+  const LsPlan p = ls_plan(k.B, k.T, k.D, kLsBwdSteps * kLsWarps);
+  const LsWs ws = ls_ws(k.workspace, p);
+  // error word, tile counter and flags (one step range: the kernel itself)
+  if (p.chunks > 1 && cudaMemsetAsync(k.workspace, 0, p.map, k.stream) != cudaSuccess)
+    return KDN_ERR_CUDA;
   linear_scan_backward_kernel<GT, XT, HAS_B, PACKED, EVEN>
-      <<<(unsigned)(p.chunks * p.cols), kLsThreads, 0, s>>>(
+      <<<(unsigned)(p.chunks * p.cols), kLsThreads, 0, k.stream>>>(
           static_cast<const GT*>(k.a), static_cast<const GT*>(k.b), static_cast<const XT*>(k.x),
-          static_cast<const XT*>(k.y), static_cast<const XT*>(k.dy), k.h0, k.dhT,
-          static_cast<GT*>(k.da), static_cast<GT*>(k.db), static_cast<XT*>(k.dx), k.dh0, k.cu, k.N,
-          k.T, k.D, (int)(p.cols / k.B), p.chunks, p.cols, ws);
+          static_cast<const XT*>(k.y), static_cast<const XT*>(k.dy), k.h0, k.end_in,
+          static_cast<GT*>(k.da), static_cast<GT*>(k.db), static_cast<XT*>(k.dx), k.end_out, k.cu,
+          k.N, k.T, k.D, (int)(p.cols / k.B), p.chunks, p.cols, ws);
   return cudaGetLastError() == cudaSuccess ? KDN_OK : KDN_ERR_CUDA;
 }
 
 template <typename GT, typename XT>
-kdn_status backward_types(const Args& k, const LsPlan& p, const LsWs& ws, cudaStream_t s) {
+kdn_status backward_types(const LsCall& k) {
   const bool even = (k.D & 1) == 0;
-#define KDN_LS_CASE(HB, PK, EV)                                    \
+#define KDN_LS_CASE(HB, PK, EV)                                          \
   if ((k.b != nullptr) == HB && (k.cu != nullptr) == PK && even == EV) \
-    return backward_launch_t<GT, XT, HB, PK, EV>(k, p, ws, s);
+    return backward_go<GT, XT, HB, PK, EV>(k);
   KDN_LS_CASE(false, false, true)
   KDN_LS_CASE(true, false, true)
   KDN_LS_CASE(false, true, true)
@@ -211,17 +208,34 @@ kdn_status linear_scan_backward_launch(const void* a, const void* b, kdn_dtype g
                                        void* da, void* db, void* dx, float* dh0, const int32_t* cu,
                                        int N, int B, int T, int D, void* workspace,
                                        cudaStream_t s) {
-  const LsPlan p = ls_plan(B, T, D, kLsBwdSteps);
-  const LsWs ws = ls_ws(workspace, p);
-  // error word, tile counter and flags (one step range: the kernel itself)
-  if (p.chunks > 1 && cudaMemsetAsync(workspace, 0, p.map, s) != cudaSuccess) return KDN_ERR_CUDA;
-  const Args k{a, b, x, y, dy, h0, dhT, da, db, dx, dh0, cu, N, B, T, D};
+  LsCall k{};
+  k.a = a;
+  k.b = b;
+  k.x = x;
+  k.y = y;
+  k.dy = dy;
+  k.gate_dtype = gate_dtype;
+  k.in_dtype = in_dtype;
+  k.h0 = h0;
+  k.end_in = dhT;
+  k.da = da;
+  k.db = db;
+  k.dx = dx;
+  k.end_out = dh0;
+  k.cu = cu;
+  k.N = N;
+  k.B = B;
+  k.T = T;
+  k.D = D;
+  k.workspace = workspace;
+  k.stream = s;
+  kdn_status st = KDN_OK;
+  if (D % 8 == 0 ? ls_stream_call<true, true>(k, &st) : ls_stream_call<true, false>(k, &st))
+    return st;
   using bf = __nv_bfloat16;
   if (gate_dtype == KDN_F32)
-    return in_dtype == KDN_F32 ? backward_types<float, float>(k, p, ws, s)
-                               : backward_types<float, bf>(k, p, ws, s);
-  return in_dtype == KDN_F32 ? backward_types<bf, float>(k, p, ws, s)
-                             : backward_types<bf, bf>(k, p, ws, s);
+    return in_dtype == KDN_F32 ? backward_types<float, float>(k) : backward_types<float, bf>(k);
+  return in_dtype == KDN_F32 ? backward_types<bf, float>(k) : backward_types<bf, bf>(k);
 }
 
 }  // namespace kdn

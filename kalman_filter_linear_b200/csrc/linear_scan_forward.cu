@@ -2,6 +2,7 @@
 // recurrence h_t = a_t h_{t-1} + b_t x_t per channel (linear_scan.cuh has the
 // tile and the look-back).
 #include "linear_scan.cuh"
+#include "linear_scan_call.h"
 
 namespace kdn {
 namespace {
@@ -186,24 +187,26 @@ kdn_status step_launch(const void* a, const void* b, const void* x, float* h, vo
 }
 
 template <typename GT, typename XT, bool HAS_B, bool PACKED, bool EVEN>
-kdn_status forward_launch(const void* a, const void* b, const void* x, const float* h0, void* y,
-                          float* h_out, const int32_t* cu, int N, int B, int T, int D,
-                          const LsPlan& p, const LsWs& ws, cudaStream_t s) {
+kdn_status forward_go(const LsCall& k) {
+  const LsPlan p = ls_plan(k.B, k.T, k.D, kLsFwdSteps * kLsWarps);
+  const LsWs ws = ls_ws(k.workspace, p);
+  // error word, tile counter and flags (one step range: the kernel itself)
+  if (p.chunks > 1 && cudaMemsetAsync(k.workspace, 0, p.map, k.stream) != cudaSuccess)
+    return KDN_ERR_CUDA;
   linear_scan_forward_kernel<GT, XT, HAS_B, PACKED, EVEN>
-      <<<(unsigned)(p.chunks * p.cols), kLsThreads, 0, s>>>(
-          static_cast<const GT*>(a), static_cast<const GT*>(b), static_cast<const XT*>(x), h0,
-          static_cast<XT*>(y), h_out, cu, N, T, D, (int)(p.cols / B), p.chunks, p.cols, ws);
+      <<<(unsigned)(p.chunks * p.cols), kLsThreads, 0, k.stream>>>(
+          static_cast<const GT*>(k.a), static_cast<const GT*>(k.b), static_cast<const XT*>(k.x),
+          k.h0, static_cast<XT*>(k.y_out), k.end_out, k.cu, k.N, k.T, k.D, (int)(p.cols / k.B),
+          p.chunks, p.cols, ws);
   return cudaGetLastError() == cudaSuccess ? KDN_OK : KDN_ERR_CUDA;
 }
 
 template <typename GT, typename XT>
-kdn_status forward_types(const void* a, const void* b, const void* x, const float* h0, void* y,
-                         float* h_out, const int32_t* cu, int N, int B, int T, int D,
-                         const LsPlan& p, const LsWs& ws, cudaStream_t s) {
-  const bool even = (D & 1) == 0;
-#define KDN_LS_CASE(HB, PK, EV)                                                             \
-  if ((b != nullptr) == HB && (cu != nullptr) == PK && even == EV)                          \
-    return forward_launch<GT, XT, HB, PK, EV>(a, b, x, h0, y, h_out, cu, N, B, T, D, p, ws, s);
+kdn_status forward_types(const LsCall& k) {
+  const bool even = (k.D & 1) == 0;
+#define KDN_LS_CASE(HB, PK, EV)                                          \
+  if ((k.b != nullptr) == HB && (k.cu != nullptr) == PK && even == EV) \
+    return forward_go<GT, XT, HB, PK, EV>(k);
   KDN_LS_CASE(false, false, true)
   KDN_LS_CASE(true, false, true)
   KDN_LS_CASE(false, true, true)
@@ -218,10 +221,9 @@ kdn_status forward_types(const void* a, const void* b, const void* x, const floa
 
 }  // namespace
 
-// of both directions (the backward's tiles are the shorter ones)
+// of both directions and any types (more and shorter tiles need more)
 size_t linear_scan_workspace_size(int B, int T, int D) {
-  const size_t f = ls_plan(B, T, D, kLsFwdSteps).bytes, b = ls_plan(B, T, D, kLsBwdSteps).bytes;
-  return f > b ? f : b;
+  return ls_plan(B, T, D, kLsShortestTile).bytes;
 }
 
 // B entries of T steps, or (cu) N sequences packed in T steps with B = 1
@@ -229,19 +231,29 @@ kdn_status linear_scan_forward_launch(const void* a, const void* b, kdn_dtype ga
                                       const void* x, kdn_dtype in_dtype, const float* h0, void* y,
                                       float* h_out, const int32_t* cu, int N, int B, int T, int D,
                                       void* workspace, cudaStream_t s) {
-  const LsPlan p = ls_plan(B, T, D, kLsFwdSteps);
-  const LsWs ws = ls_ws(workspace, p);
-  // error word, tile counter and flags (one step range: the kernel itself)
-  if (p.chunks > 1 && cudaMemsetAsync(workspace, 0, p.map, s) != cudaSuccess) return KDN_ERR_CUDA;
-  if (gate_dtype == KDN_F32) {
-    if (in_dtype == KDN_F32)
-      return forward_types<float, float>(a, b, x, h0, y, h_out, cu, N, B, T, D, p, ws, s);
-    return forward_types<float, __nv_bfloat16>(a, b, x, h0, y, h_out, cu, N, B, T, D, p, ws, s);
-  }
-  if (in_dtype == KDN_F32)
-    return forward_types<__nv_bfloat16, float>(a, b, x, h0, y, h_out, cu, N, B, T, D, p, ws, s);
-  return forward_types<__nv_bfloat16, __nv_bfloat16>(a, b, x, h0, y, h_out, cu, N, B, T, D, p, ws,
-                                                     s);
+  LsCall k{};
+  k.a = a;
+  k.b = b;
+  k.x = x;
+  k.gate_dtype = gate_dtype;
+  k.in_dtype = in_dtype;
+  k.h0 = h0;
+  k.y_out = y;
+  k.end_out = h_out;
+  k.cu = cu;
+  k.N = N;
+  k.B = B;
+  k.T = T;
+  k.D = D;
+  k.workspace = workspace;
+  k.stream = s;
+  kdn_status st = KDN_OK;
+  if (D % 8 == 0 ? ls_stream_call<false, true>(k, &st) : ls_stream_call<false, false>(k, &st))
+    return st;
+  using bf = __nv_bfloat16;
+  if (gate_dtype == KDN_F32)
+    return in_dtype == KDN_F32 ? forward_types<float, float>(k) : forward_types<float, bf>(k);
+  return in_dtype == KDN_F32 ? forward_types<bf, float>(k) : forward_types<bf, bf>(k);
 }
 
 kdn_status linear_scan_step_launch(const void* a, const void* b, kdn_dtype gate_dtype,

@@ -1,0 +1,6 @@
+// The streamed forward kernels for rows of any length.
+#include "linear_scan_stream.cuh"
+
+namespace kdn {
+template bool ls_stream_call<false, false>(const LsCall&, kdn_status*);
+}  // namespace kdn

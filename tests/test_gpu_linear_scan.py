@@ -288,6 +288,88 @@ def test_streams_and_a_replayed_graph():
         assert all(torch.equal(g[k], grads[i][k]) for k in g)
 
 
+@pytest.mark.parametrize("gate,dt,with_b", [(F32, F32, True), (F32, BF16, False), (BF16, BF16, True),
+                                            (BF16, F32, False)])
+@pytest.mark.parametrize("D", [8, 9, 24, 57, 64, 71, 136, 201])
+@pytest.mark.parametrize("B,T", [(1, 7), (1, 8), (3, 9), (2, 64), (3, 65), (1, 127), (2, 515)])
+def test_rows_of_whole_pieces_and_others(gate, dt, with_b, D, B, T):
+    """Rows on 16-byte boundaries and not, a last line of fewer than eight rows,
+    tiles that end a sequence early."""
+    a, x, b, h0 = _inputs((B, T, D), (B, D), gate, dt, with_b, seed=B * 1000 + T + D)
+    y, h = kdn.kdn_linear_scan_forward(a, x, b=b, h0=h0)
+    _check_forward(a, x, b, h0, y, h, [(s, s) for s in range(B)])
+    gen = torch.Generator().manual_seed(11)
+    dy = torch.randn((B, T, D), generator=gen).to(dt).cuda()
+    dh = torch.randn((B, D), generator=gen).cuda()
+    g = kdn.kdn_linear_scan_backward(a, x if with_b else None, y, dy, b=b, h0=h0, dh_T=dh)
+    _check_backward(a, x, b, h0, y, dy, dh, g, [(s, s) for s in range(B)])
+
+
+@pytest.mark.parametrize("B,T,D", [(700, 70, 64), (90, 150, 515), (1, 3000, 200), (2, 1200, 640)])
+def test_many_columns_and_few(B, T, D):
+    """More columns of 64 channels than run at once, and so few that several
+    blocks share one."""
+    a, x, b, h0 = _inputs((B, T, D), (B, D), F32, F32, True, seed=B)
+    y, h = kdn.kdn_linear_scan_forward(a, x, b=b, h0=h0)
+    some = sorted({0, B // 2, B - 1})
+    _check_forward(a, x, b, h0, y, h, [(s, s) for s in some])
+    dh = torch.randn((B, D), device='cuda')
+    g = kdn.kdn_linear_scan_backward(a, x, y, x, b=b, h0=h0, dh_T=dh)
+    _check_backward(a, x, b, h0, y, x, dh, g, [(s, s) for s in some])
+    # every entry by itself gives the same bits
+    for s in some:
+        a1, x1, b1, y0, s1, d1 = (t[s:s + 1].clone() for t in (a, x, b, y, h0, dh))
+        y1, h1 = kdn.kdn_linear_scan_forward(a1, x1, b=b1, h0=s1)
+        assert torch.equal(y1, y0) and torch.equal(h1, h[s:s + 1])
+        g1 = kdn.kdn_linear_scan_backward(a1, x1, y0, x1, b=b1, h0=s1, dh_T=d1)
+        assert all(torch.equal(g1[k], g[k][s:s + 1]) for k in g)
+
+
+@pytest.mark.parametrize("D", [64, 67, 320, 2048])
+@pytest.mark.parametrize("T", [50, 300, 1000, 2500])
+def test_states_in_place(D, T):
+    """h_out on h0 and dh0 on dh_T, dense and packed, give the bits of separate
+    memory."""
+    a, x, b, h0 = _inputs((2, T, D), (2, D), F32, BF16, True, seed=T + D)
+    cu = _packed([T // 3, 0, T - T // 3 - 5, 5])
+    states = torch.randn(4, D, device='cuda')
+    for args, s0, kw in (((a, x), h0, {}), ((a[0], x[0]), states, dict(cu_seqlens=cu))):
+        bb = b if not kw else b[0]
+        y, h = kdn.kdn_linear_scan_forward(*args, b=bb, h0=s0, **kw)
+        g = kdn.kdn_linear_scan_backward(*args, y, args[1], b=bb, h0=s0, dh_T=s0, **kw)
+        for _ in range(3):
+            st = s0.clone()
+            y2, h2 = kdn.kdn_linear_scan_forward(*args, b=bb, h0=st, h_out=st, **kw)
+            d2 = s0.clone()
+            g2 = kdn.kdn_linear_scan_backward(*args, y, args[1], b=bb, h0=s0, dh_T=d2, dh0=d2, **kw)
+            if kw:  # (the two may run in different tiles)
+                torch.testing.assert_close(h2, h, rtol=1e-5, atol=1e-5)
+                torch.testing.assert_close(y2.float(), y.float(), rtol=2 ** -7, atol=1e-5)
+                torch.testing.assert_close(g2['h0'], g['h0'], rtol=1e-5, atol=1e-5)
+            else:
+                assert torch.equal(y2, y) and torch.equal(h2, h)
+                assert all(torch.equal(g2[k], g[k]) for k in g)
+
+
+def test_packed_boundaries_at_every_place():
+    """Sequences of 1 to 40 steps, and pairs of boundaries at every distance
+    within a warp's steps."""
+    D = 64
+    for lengths in ([n for n in range(1, 41)], [n for n in range(40, 0, -1)] + [0, 0, 64, 0],
+                    [16] * 20, [8, 24, 1, 31, 2, 30, 15, 17] * 6):
+        N, T = len(lengths), sum(lengths)
+        for gate, dt, width in ((F32, F32, D), (BF16, BF16, D), (F32, BF16, 37)):
+            a, x, b, h0 = _inputs((T, width), (N, width), gate, dt, True, seed=N)
+            ends = np.cumsum(lengths)
+            ranges = [(slice(int(e - n), int(e)), s) for s, (n, e) in enumerate(zip(lengths, ends))]
+            y, h = kdn.kdn_linear_scan_forward(a, x, b=b, h0=h0, cu_seqlens=_packed(lengths))
+            _check_forward(a, x, b, h0, y, h, ranges)
+            dh = torch.randn_like(h)
+            g = kdn.kdn_linear_scan_backward(a, x, y, x, b=b, h0=h0, dh_T=dh,
+                                             cu_seqlens=_packed(lengths))
+            _check_backward(a, x, b, h0, y, x, dh, g, ranges)
+
+
 def test_refusals():
     a, x, b, h0 = _inputs((2, 30, 64), (2, 64), F32, BF16, True, seed=1)
     with pytest.raises(TypeError):
