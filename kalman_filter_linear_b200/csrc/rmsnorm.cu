@@ -9,9 +9,16 @@
 //   dw = sum over rows of dy h rs.
 //
 // One read of every input and one write of every output: a row stays in
-// registers between its reduction and its use.  Thread t of a row's G threads
-// holds elements [8 (t + G v), 8 (t + G v) + 8), so loads are 16 bytes a
-// thread and a block of 128 is a half warp's.
+// registers between its reduction and its use, and the next row's loads are
+// under way meanwhile.  Rows are taken in turn by as many blocks as stay on the
+// device at once (one row a block of its own leaves each SM waiting at the
+// rows' starts and ends: 268 us in place of 90 for 32768 rows of 2048, fp32
+// in, e4m3 out).  A row has G threads.
+// VEC (rows of a multiple of 8): thread t holds the elements [8 (t + G v),
+// 8 (t + G v) + 8), so loads are 16 bytes a thread and a block of 128 is a half
+// warp's.  Otherwise rows do not start on 16-byte boundaries: a warp holds 256
+// elements, lane l those at l, l + 32, ..., so that loads of single elements are
+// consecutive, and a block of 128 is a warp's.
 #include "fp8_common.cuh"
 
 namespace kdn {
@@ -19,216 +26,332 @@ namespace {
 
 enum class Out { F32, BF16, E4M3 };
 
-// Sums of `x` over a row's G threads, in all of them (G = 32: a warp).
-template <int G>
-__device__ __forceinline__ float row_sum(float x, float* sh) {
-  x = warp_sum(x);
+// A thread's eight elements of a row, as they were loaded.
+template <typename T, bool VEC>
+struct Held {
+  float v[8];
+  template <int G>
+  __device__ __forceinline__ void load(const T* row, int t, int vth, int D) {
+    if constexpr (VEC) {
+      const int e = 8 * (t + G * vth);
+      load8(row + e, D - e, true, v);
+    } else {
+      const int e = 256 * ((t >> 5) + G / 32 * vth) + (t & 31);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = e + 32 * i < D ? to_f32<T>(row[e + 32 * i]) : 0.f;
+    }
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = v[i];
+  }
+};
+template <>
+struct Held<__nv_bfloat16, true> {
+  uint4 w;
+  template <int G>
+  __device__ __forceinline__ void load(const __nv_bfloat16* row, int t, int vth, int D) {
+    const int e = 8 * (t + G * vth);
+    w = e < D ? __ldg(reinterpret_cast<const uint4*>(row + e)) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const { unpack_bf16x8(w, x); }
+};
+__device__ __forceinline__ void put1(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+template <int G, bool VEC, typename T>
+__device__ __forceinline__ void put(T* row, int t, int vth, int D, const float (&x)[8]) {
+  if constexpr (VEC) {
+    const int e = 8 * (t + G * vth);
+    store8(row + e, D - e, true, x);
+  } else {
+    const int e = 256 * ((t >> 5) + G / 32 * vth) + (t & 31);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (e + 32 * i < D) put1(row + e + 32 * i, x[i]);
+  }
+}
+
+// Threads of a block, and the blocks of an SM that registers allow.
+template <int G, int NV, bool VEC>
+struct Shape {
+  static constexpr int THREADS = G < 256 ? 256 : G;
+  static constexpr int ROWS = THREADS / G;  // of a block at once
+  static constexpr int FWD = NV == 2 && VEC ? 512 : NV > 2 ? 512 : 1024;  // threads of an SM
+  static constexpr int BWD = G == 1024 ? 1024 : NV > 1 ? 512 : 768;
+  static constexpr int BLOCKS = FWD / THREADS, BWD_BLOCKS = BWD / THREADS;
+};
+
+// Sums over a row's G threads, in all of them.  Two buffers in turn: a slow
+// warp may still read the last row's sums.
+template <int G, int N>
+__device__ __forceinline__ void row_sums(float (&x)[N], float (*sh)[N], int turn, int warps) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = warp_sum(x[i]);
   if constexpr (G > 32) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (lane == 0) sh[warp] = x;
+    if (lane == 0)
+#pragma unroll
+      for (int i = 0; i < N; ++i) sh[turn * warps + warp][i] = x[i];
     __syncthreads();
-    x = 0.f;
+    const int w0 = turn * warps + (warp & ~(G / 32 - 1));
 #pragma unroll
-    for (int w = 0; w < G / 32; ++w) x += sh[w];
+    for (int i = 0; i < N; ++i) x[i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < G / 32; ++w)
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] += sh[w0 + w][i];
   }
-  return x;
 }
 
-template <typename XT, typename RT, Out OUT, int G, int NV>
-__global__ void __launch_bounds__(256)
-rmsnorm_forward_kernel(const XT* __restrict__ X, const RT* __restrict__ Res,
-                       const float* __restrict__ W, RT* __restrict__ Hout,
-                       void* __restrict__ Yv, float* __restrict__ Scale, int64_t rows, int D,
-                       int64_t ldy, float eps, int vec) {
-  __shared__ float sh[8];
+template <typename XT, typename RT, bool RES, Out OUT, int G, int NV, bool VEC>
+__global__ void __launch_bounds__(Shape<G, NV, VEC>::THREADS, Shape<G, NV, VEC>::BLOCKS)
+rmsnorm_forward_kernel(const XT* __restrict__ X, const RT* Res, const float* __restrict__ W,
+                       RT* Hout, void* __restrict__ Yv, float* __restrict__ Scale, int64_t rows,
+                       int D, int64_t ldy, float eps) {
+  using S = Shape<G, NV, VEC>;
+  constexpr int WARPS = S::THREADS / 32;
+  __shared__ float sh[2 * WARPS][1];
   const int t = threadIdx.x % G;
-  const int64_t row = G == 32 ? (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32
-                              : (int64_t)blockIdx.x;
-  if (row >= rows) return;  // (whole warps or the whole block)
-  float h[NV][8];
-  const XT* x = X + row * D;
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int e = 8 * (t + G * v);
-    load8(x + e, min(8, D - e), vec, h[v]);
-  }
-  if (Res) {
-    const RT* r = Res + row * D;
-    float q[NV][8];
+  const int64_t step = (int64_t)gridDim.x * S::ROWS;
+  int64_t row = (int64_t)blockIdx.x * S::ROWS + threadIdx.x / G;
+  Held<XT, VEC> x[NV];
+  Held<RT, VEC> r[NV];
+  auto fetch = [&](int64_t from) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int e = 8 * (t + G * v);
-      load8(r + e, min(8, D - e), vec, q[v]);
+      x[v].template load<G>(X + from * D, t, v, D);
+      if (RES) r[v].template load<G>(Res + from * D, t, v, D);
     }
+  };
+  constexpr bool AHEAD = VEC;
+  if (AHEAD && row < rows) fetch(row);
+  float w[NV][8];
+  if (NV < 4) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int e = 8 * (t + G * v);
+      Held<float, VEC> h;
+      h.template load<G>(W, t, v, D);
+      h.get(w[v]);
+    }
+  }
+  int turn = 0;
+  // (all threads of a block go round together: a row's sums meet at a barrier)
+  for (int64_t first = (int64_t)blockIdx.x * S::ROWS; first < rows;
+       first += step, row += step, turn ^= 1) {
+    const bool have = row < rows;
+    if (!AHEAD && have) fetch(row);
+    float h[NV][8], ss[1] = {0.f};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        h[v][i] += q[v][i];
-        if (sizeof(RT) == 2) h[v][i] = __bfloat162float(__float2bfloat16_rn(h[v][i]));
+    for (int v = 0; v < NV; ++v) {
+      x[v].get(h[v]);
+      if (RES) {
+        float q[8];
+        r[v].get(q);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          h[v][i] += q[i];
+          if (sizeof(RT) == 2) h[v][i] = __bfloat162float(__float2bfloat16_rn(h[v][i]));
+        }
+        if (have) put<G, VEC>(Hout + row * D, t, v, D, h[v]);
       }
-      if (Hout) store8(Hout + row * D + e, min(8, D - e), vec, h[v]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss[0] = fmaf(h[v][i], h[v][i], ss[0]);
     }
-  }
-  float ss = 0.f;
+    if (AHEAD && row + step < rows) fetch(row + step);
+    row_sums<G>(ss, sh, turn, WARPS);
+    const float rs = rsqrtf(ss[0] / (float)D + eps);
 #pragma unroll
-  for (int v = 0; v < NV; ++v)
+    for (int v = 0; v < NV; ++v) {
+      if (NV >= 4) {
+        Held<float, VEC> hw;
+        hw.template load<G>(W, t, v, D);
+        hw.get(w[v]);
+      }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(h[v][i], h[v][i], ss);
-  ss = row_sum<G>(ss, sh);
-  const float rs = rsqrtf(ss / (float)D + eps);
+      for (int i = 0; i < 8; ++i) h[v][i] = h[v][i] * rs * w[v][i];
+      if (OUT == Out::F32) {
+        if (have) put<G, VEC>(static_cast<float*>(Yv) + row * D, t, v, D, h[v]);
+      } else if (OUT == Out::BF16) {
+        if (have) put<G, VEC>(static_cast<__nv_bfloat16*>(Yv) + row * D, t, v, D, h[v]);
+      } else if constexpr (VEC) {
+        // elements behind the row's end are zeros here: they do not raise the
+        // maximum
+        const int e = 8 * (t + G * v);
+        const float top = half_warp_max(amax8(h[v]));
+        const float inv = fp8_inverse(top);
+        if (have && e < D) {
+          uint2 c;
+          c.x = fp8_pack4(h[v][0], h[v][1], h[v][2], h[v][3], inv);
+          c.y = fp8_pack4(h[v][4], h[v][5], h[v][6], h[v][7], inv);
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(Yv) + row * ldy + e) = c;
+          if ((t & 15) == 0) Scale[row * ((D + 127) / 128) + e / 128] = fp8_scale(top);
+        }
+      } else {
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int e = 8 * (t + G * v);
-    const int n = min(8, D - e);
-    float w[8];
-    load8(W + e, n, vec, w);
+        for (int half = 0; half < 2; ++half) {
+          const float(&q)[8] = h[v];
+          const int e = 256 * ((t >> 5) + G / 32 * v) + 128 * half + (t & 31);
+          float top = fabsf(q[4 * half]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[v][i] = h[v][i] * rs * w[i];
-    if (OUT == Out::F32) {
-      store8(static_cast<float*>(Yv) + row * D + e, n, vec, h[v]);
-    } else if (OUT == Out::BF16) {
-      store8(static_cast<__nv_bfloat16*>(Yv) + row * D + e, n, vec, h[v]);
-    } else {
-      // elements behind the row's end are zeros here: they do not raise the
-      // maximum, and their codes fall into the row's padding
-      const float top = half_warp_max(amax8(h[v]));
-      const float inv = fp8_inverse(top);
-      if (n > 0) {
-        uint2 c;
-        c.x = fp8_pack4(h[v][0], h[v][1], h[v][2], h[v][3], inv);
-        c.y = fp8_pack4(h[v][4], h[v][5], h[v][6], h[v][7], inv);
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(Yv) + row * ldy + e) = c;
-        if ((t & 15) == 0) Scale[row * ((D + 127) / 128) + e / 128] = fp8_scale(top);
+          for (int i = 1; i < 4; ++i) top = max_nan(top, fabsf(q[4 * half + i]));
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1)
+            top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const uint32_t c = fp8_pack4(q[4 * half], q[4 * half + 1], q[4 * half + 2],
+                                       q[4 * half + 3], fp8_inverse(top));
+          uint8_t* y = static_cast<uint8_t*>(Yv) + row * ldy + e;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (have && e + 32 * i < D) y[32 * i] = (uint8_t)(c >> (8 * i));
+          if (have && (t & 31) == 0 && e < D)
+            Scale[row * ((D + 127) / 128) + e / 128] = fp8_scale(top);
+        }
       }
     }
   }
 }
 
-constexpr int kNormBwdBlocks = 592;  // 4 a SM: rows are taken in turn
+constexpr int kNormBwdBlocks = 592;  // most that write a part of dw
 
-template <typename HT, typename YT, typename XT, int G, int NV>
-__global__ void __launch_bounds__(256)
+// A thread holds its elements as they were loaded, through the reduction, and
+// with VEC, up to rows of 8192, the next row's too.
+template <typename HT, typename YT, typename XT, int G, int NV, bool VEC>
+__global__ void __launch_bounds__(Shape<G, NV, VEC>::THREADS, Shape<G, NV, VEC>::BWD_BLOCKS)
 rmsnorm_backward_kernel(const HT* __restrict__ Hin, const float* __restrict__ W,
-                        const YT* __restrict__ dY, const HT* __restrict__ dH,
-                        XT* __restrict__ dX, HT* __restrict__ dRes, float* __restrict__ part,
-                        int64_t rows, int D, float eps, int vec) {
-  __shared__ float sh[2][16];
-  extern __shared__ float acc_sh[];  // G = 32: one row of sums a warp
-  const int t = threadIdx.x % G, warp = threadIdx.x >> 5;
-  constexpr int kRowsPerBlock = 256 / G;
-  float acc[NV][8];
+                        const YT* __restrict__ dY, const HT* dH, XT* __restrict__ dX, HT* dRes,
+                        float* __restrict__ part, int64_t rows, int D, float eps) {
+  using S = Shape<G, NV, VEC>;
+  constexpr int WARPS = S::THREADS / 32;
+  constexpr bool AHEAD = G < 1024 && VEC, KEEP = G < 1024;  // KEEP: the weights
+  __shared__ float sh[2 * WARPS][2];
+  extern __shared__ float acc_sh[];  // several rows a block: [row][D] sums
+  const int t = threadIdx.x % G;
+  const int64_t step = (int64_t)gridDim.x * S::ROWS;
+  int64_t row = (int64_t)blockIdx.x * S::ROWS + threadIdx.x / G;
+  struct Row {
+    Held<HT, VEC> h, d;
+    Held<YT, VEC> g;
+  };
+  Row now[NV], ahead[AHEAD ? NV : 1];
+  float acc[NV][8], w[KEEP ? NV : 1][8];
 #pragma unroll
   for (int v = 0; v < NV; ++v)
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[v][i] = 0.f;
-  const int64_t step = (int64_t)gridDim.x * kRowsPerBlock;
+  auto weights = [&](int v, float (&x)[8]) {
+    Held<float, VEC> h;
+    h.template load<G>(W, t, v, D);
+    h.get(x);
+  };
+  auto fetch = [&](Row& r, int64_t from, int v) {
+    r.h.template load<G>(Hin + from * D, t, v, D);
+    r.g.template load<G>(dY + from * D, t, v, D);
+    if (dH) r.d.template load<G>(dH + from * D, t, v, D);
+  };
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    if (KEEP) weights(v, w[KEEP ? v : 0]);
+    if (AHEAD && row < rows) fetch(ahead[AHEAD ? v : 0], row, v);
+  }
   int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * kRowsPerBlock + (G == 32 ? warp : 0); row < rows;
-       row += step, turn ^= 1) {
-    float h[NV][8], g[NV][8];
-    float ss = 0.f, sg = 0.f;
+  for (int64_t first = (int64_t)blockIdx.x * S::ROWS; first < rows;
+       first += step, row += step, turn ^= 1) {
+    const bool have = row < rows;
+    float sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int e = 8 * (t + G * v);
-      load8(Hin + row * D + e, min(8, D - e), vec, h[v]);
-      load8(dY + row * D + e, min(8, D - e), vec, g[v]);
+      if (AHEAD) {
+        now[v] = ahead[AHEAD ? v : 0];
+        if (row + step < rows) fetch(ahead[AHEAD ? v : 0], row + step, v);
+      } else if (have) {
+        fetch(now[v], row, v);
+      }
     }
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int e = 8 * (t + G * v);
-      float w[8];
-      load8(W + e, min(8, D - e), vec, w);
+      float h[8], g[8];
+      now[v].h.get(h);
+      now[v].g.get(g);
+      if (!KEEP) weights(v, w[0]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        ss = fmaf(h[v][i], h[v][i], ss);
-        sg = fmaf(g[v][i] * w[i], h[v][i], sg);
+        sum[0] = fmaf(h[i], h[i], sum[0]);
+        sum[1] = fmaf(g[i] * w[KEEP ? v : 0][i], h[i], sum[1]);
       }
     }
-    ss = warp_sum(ss);
-    sg = warp_sum(sg);
-    if constexpr (G > 32) {
-      // two buffers in turn: a slow warp may still read the last row's sums
-      if ((threadIdx.x & 31) == 0) {
-        sh[turn][2 * warp] = ss;
-        sh[turn][2 * warp + 1] = sg;
-      }
-      __syncthreads();
-      ss = sg = 0.f;
+    row_sums<G>(sum, sh, turn, WARPS);
+    const float rs = rsqrtf(sum[0] / (float)D + eps);
+    const float k = rs * rs * (sum[1] / (float)D);
+    if (have) {
 #pragma unroll
-      for (int w = 0; w < G / 32; ++w) {
-        ss += sh[turn][2 * w];
-        sg += sh[turn][2 * w + 1];
-      }
-    }
-    const float rs = rsqrtf(ss / (float)D + eps);
-    const float k = rs * rs * (sg / (float)D);
+      for (int v = 0; v < NV; ++v) {
+        if (!KEEP) weights(v, w[0]);
+        float h[8], g[8], d[8];
+        now[v].h.get(h);
+        now[v].g.get(g);
+        if (dH) {
+          now[v].d.get(d);
+        } else {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int e = 8 * (t + G * v);
-      const int n = min(8, D - e);
-      float w[8], d[8];
-      load8(W + e, n, vec, w);
-      if (dH) {
-        load8(dH + row * D + e, n, vec, d);
-      } else {
+          for (int i = 0; i < 8; ++i) d[i] = 0.f;
+        }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = 0.f;
+        for (int i = 0; i < 8; ++i) {
+          acc[v][i] = fmaf(g[i], h[i] * rs, acc[v][i]);
+          d[i] += rs * (g[i] * w[KEEP ? v : 0][i] - h[i] * k);
+        }
+        put<G, VEC>(dX + row * D, t, v, D, d);
+        if (dRes) put<G, VEC>(dRes + row * D, t, v, D, d);
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        acc[v][i] = fmaf(g[v][i], h[v][i] * rs, acc[v][i]);
-        d[i] += rs * (g[v][i] * w[i] - h[v][i] * k);
-      }
-      store8(dX + row * D + e, n, vec, d);
-      if (dRes) store8(dRes + row * D + e, n, vec, d);
     }
   }
   // this block's part of dw
   float* out = part + (int64_t)blockIdx.x * D;
-  if constexpr (G > 32) {
+  if constexpr (S::ROWS == 1) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int e = 8 * (t + G * v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (e + i < D) out[e + i] = acc[v][i];
-    }
+    for (int v = 0; v < NV; ++v) put<G, VEC>(out, t, v, D, acc[v]);
   } else {
+    float* mine = acc_sh + threadIdx.x / G * D;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int e = 8 * (t + G * v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (e + i < D) acc_sh[warp * D + e + i] = acc[v][i];
+      for (int i = 0; i < 8; ++i) {
+        const int e = VEC ? 8 * (t + G * v) + i : 256 * ((t >> 5) + G / 32 * v) + (t & 31) + 32 * i;
+        if (e < D) mine[e] = acc[v][i];
+      }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < D; e += 256) {
+    for (int e = threadIdx.x; e < D; e += S::THREADS) {
       float s = 0.f;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) s += acc_sh[w * D + e];
+      for (int r = 0; r < S::ROWS; ++r) s += acc_sh[r * D + e];
       out[e] = s;
     }
   }
 }
 
-// dw = the sum of the blocks' parts, in a fixed order: 32 columns a block, 8
-// threads a column
-__global__ void __launch_bounds__(256)
+// dw = the sum of the blocks' parts, in a fixed order: 32 columns a block, 32
+// threads a column, each with every 32nd part
+__global__ void __launch_bounds__(1024)
 rmsnorm_dweight_kernel(const float* __restrict__ part, float* __restrict__ dw, int parts, int D) {
-  __shared__ float sh[8][32];
+  __shared__ float sh[32][33];
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), r = threadIdx.x >> 5;
-  float s = 0.f;
-  if (c < D)
-    for (int p = r; p < parts; p += 8) s += part[(int64_t)p * D + c];
-  sh[r][threadIdx.x & 31] = s;
-  __syncthreads();
-  if (r == 0 && c < D) {
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  if (c < D) {
+    for (int p = r; p < parts; p += 128) {
+      float x[4];
 #pragma unroll
-    for (int k = 1; k < 8; ++k) s += sh[k][threadIdx.x & 31];
-    dw[c] = s;
+      for (int i = 0; i < 4; ++i)
+        x[i] = p + 32 * i < parts ? __ldg(part + (int64_t)(p + 32 * i) * D + c) : 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] += x[i];
+    }
   }
+  sh[r][threadIdx.x & 31] = (s[0] + s[1]) + (s[2] + s[3]);
+  __syncthreads();
+  // warp r adds column r's 32 sums
+  const float total = warp_sum(sh[threadIdx.x & 31][r]);
+  if ((threadIdx.x & 31) == 0 && blockIdx.x * 32 + r < D) dw[blockIdx.x * 32 + r] = total;
 }
 
 struct FwdArgs {
@@ -242,38 +365,46 @@ struct FwdArgs {
   float eps;
 };
 
-template <typename XT, typename RT, Out OUT, int G, int NV>
-kdn_status fwd_go(const FwdArgs& a, cudaStream_t s) {
-  // a warp's row: as many warps a block as still give every SM a block
-  int warps = 8;
-  if (G == 32)
-    while (warps > 1 && (a.rows + warps - 1) / warps < 148) warps >>= 1;
-  const int threads = G == 32 ? 32 * warps : G;
-  const int64_t blocks = G == 32 ? (a.rows + warps - 1) / warps : a.rows;
-  rmsnorm_forward_kernel<XT, RT, OUT, G, NV><<<(unsigned)blocks, threads, 0, s>>>(
-      static_cast<const XT*>(a.x), static_cast<const RT*>(a.res), a.w, static_cast<RT*>(a.h), a.y,
-      a.scale, a.rows, a.D, a.ldy, a.eps, a.D % 8 == 0);
-  return cudaGetLastError() == cudaSuccess ? KDN_OK : KDN_ERR_CUDA;
-}
-// A row of up to 2048 goes to one warp (no barrier), a longer one to 256
-// threads.
-template <typename XT, typename RT, Out OUT>
-kdn_status fwd_size(const FwdArgs& a, cudaStream_t s) {
-  if (a.D <= 256) return fwd_go<XT, RT, OUT, 32, 1>(a, s);
-  if (a.D <= 512) return fwd_go<XT, RT, OUT, 32, 2>(a, s);
-  if (a.D <= 1024) return fwd_go<XT, RT, OUT, 32, 4>(a, s);
-  if (a.D <= 2048) return fwd_go<XT, RT, OUT, 32, 8>(a, s);
-  if (a.D <= 4096) return fwd_go<XT, RT, OUT, 256, 2>(a, s);
-  if (a.D <= 8192) return fwd_go<XT, RT, OUT, 256, 4>(a, s);
-  return fwd_go<XT, RT, OUT, 256, 8>(a, s);
-}
-template <typename XT, typename RT>
-kdn_status fwd_out(const FwdArgs& a, kdn_dtype out, cudaStream_t s) {
-  if (out == KDN_F32) return fwd_size<XT, RT, Out::F32>(a, s);
-  if (out == KDN_BF16) return fwd_size<XT, RT, Out::BF16>(a, s);
-  return fwd_size<XT, RT, Out::E4M3>(a, s);
+inline int64_t resident(int per_sm) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return (int64_t)sms * per_sm;
 }
 
+template <typename XT, typename RT, bool RES, Out OUT, int G, int NV, bool VEC>
+kdn_status fwd_go(const FwdArgs& a, cudaStream_t s) {
+  using S = Shape<G, NV, VEC>;
+  const int64_t want = (a.rows + S::ROWS - 1) / S::ROWS, most = resident(S::BLOCKS);
+  if (most == 0) return KDN_ERR_CUDA;
+  rmsnorm_forward_kernel<XT, RT, RES, OUT, G, NV, VEC>
+      <<<(unsigned)(want < most ? want : most), S::THREADS, 0, s>>>(
+          static_cast<const XT*>(a.x), static_cast<const RT*>(a.res), a.w, static_cast<RT*>(a.h),
+          a.y, a.scale, a.rows, a.D, a.ldy, a.eps);
+  return cudaGetLastError() == cudaSuccess ? KDN_OK : KDN_ERR_CUDA;
+}
+template <typename XT, typename RT, bool RES, Out OUT, bool VEC>
+kdn_status fwd_size(const FwdArgs& a, cudaStream_t s) {
+  if (a.D <= 256) return fwd_go<XT, RT, RES, OUT, 32, 1, VEC>(a, s);
+  if (a.D <= 512) return fwd_go<XT, RT, RES, OUT, 64, 1, VEC>(a, s);
+  if (a.D <= 1024) return fwd_go<XT, RT, RES, OUT, 128, 1, VEC>(a, s);
+  if (a.D <= 2048) return fwd_go<XT, RT, RES, OUT, 256, 1, VEC>(a, s);
+  if (a.D <= 4096) return fwd_go<XT, RT, RES, OUT, 512, 1, VEC>(a, s);
+  if (a.D <= 8192) return fwd_go<XT, RT, RES, OUT, 512, 2, VEC>(a, s);
+  return fwd_go<XT, RT, RES, OUT, 512, 4, VEC>(a, s);
+}
+template <typename XT, typename RT, bool RES, bool VEC>
+kdn_status fwd_out(const FwdArgs& a, kdn_dtype out, cudaStream_t s) {
+  if (out == KDN_F32) return fwd_size<XT, RT, RES, Out::F32, VEC>(a, s);
+  if (out == KDN_BF16) return fwd_size<XT, RT, RES, Out::BF16, VEC>(a, s);
+  return fwd_size<XT, RT, RES, Out::E4M3, VEC>(a, s);
+}
+template <typename XT, typename RT, bool RES>
+kdn_status fwd_vec(const FwdArgs& a, kdn_dtype out, cudaStream_t s) {
+  return a.D % 8 == 0 ? fwd_out<XT, RT, RES, true>(a, out, s)
+                      : fwd_out<XT, RT, RES, false>(a, out, s);
+}
 struct BwdArgs {
   const void* h;
   const float* w;
@@ -285,35 +416,42 @@ struct BwdArgs {
   float eps;
 };
 
-template <typename HT, typename YT, typename XT, int G, int NV>
+template <typename HT, typename YT, typename XT, int G, int NV, bool VEC>
 kdn_status bwd_go(const BwdArgs& a, cudaStream_t s) {
-  const int64_t per = 256 / G;
-  const int64_t want = (a.rows + per - 1) / per;
-  const int blocks = (int)(want < kNormBwdBlocks ? want : kNormBwdBlocks);
-  const size_t smem = G == 32 ? (size_t)8 * a.D * 4 : 0;
+  using S = Shape<G, NV, VEC>;
+  const int64_t want = (a.rows + S::ROWS - 1) / S::ROWS;
+  int64_t most = resident(S::BWD_BLOCKS);
+  if (most == 0) return KDN_ERR_CUDA;
+  if (most > kNormBwdBlocks) most = kNormBwdBlocks;
+  const int blocks = (int)(want < most ? want : most);
+  const size_t smem = S::ROWS > 1 ? (size_t)S::ROWS * a.D * 4 : 0;
   if (blocks > 0) {
-    rmsnorm_backward_kernel<HT, YT, XT, G, NV><<<blocks, 256, smem, s>>>(
+    rmsnorm_backward_kernel<HT, YT, XT, G, NV, VEC><<<blocks, S::THREADS, smem, s>>>(
         static_cast<const HT*>(a.h), a.w, static_cast<const YT*>(a.dy),
         static_cast<const HT*>(a.dh), static_cast<XT*>(a.dx), static_cast<HT*>(a.dres), a.part,
-        a.rows, a.D, a.eps, a.D % 8 == 0);
+        a.rows, a.D, a.eps);
     if (cudaGetLastError() != cudaSuccess) return KDN_ERR_CUDA;
   }
-  rmsnorm_dweight_kernel<<<(a.D + 31) / 32, 256, 0, s>>>(a.part, a.dw, blocks, a.D);
+  rmsnorm_dweight_kernel<<<(a.D + 31) / 32, 1024, 0, s>>>(a.part, a.dw, blocks, a.D);
   return cudaGetLastError() == cudaSuccess ? KDN_OK : KDN_ERR_CUDA;
 }
-template <typename HT, typename YT, typename XT>
+template <typename HT, typename YT, typename XT, bool VEC>
 kdn_status bwd_size(const BwdArgs& a, cudaStream_t s) {
-  if (a.D <= 256) return bwd_go<HT, YT, XT, 32, 1>(a, s);
-  if (a.D <= 512) return bwd_go<HT, YT, XT, 32, 2>(a, s);
-  if (a.D <= 1024) return bwd_go<HT, YT, XT, 32, 4>(a, s);
-  if (a.D <= 2048) return bwd_go<HT, YT, XT, 256, 1>(a, s);
-  if (a.D <= 4096) return bwd_go<HT, YT, XT, 256, 2>(a, s);
-  if (a.D <= 8192) return bwd_go<HT, YT, XT, 256, 4>(a, s);
-  return bwd_go<HT, YT, XT, 256, 8>(a, s);
+  if (a.D <= 256) return bwd_go<HT, YT, XT, 32, 1, VEC>(a, s);
+  if (a.D <= 512) return bwd_go<HT, YT, XT, 64, 1, VEC>(a, s);
+  if (a.D <= 1024) return bwd_go<HT, YT, XT, 128, 1, VEC>(a, s);
+  if (a.D <= 2048) return bwd_go<HT, YT, XT, 256, 1, VEC>(a, s);
+  if (a.D <= 4096) return bwd_go<HT, YT, XT, 256, 2, VEC>(a, s);
+  if (a.D <= 8192) return bwd_go<HT, YT, XT, 512, 2, VEC>(a, s);
+  return bwd_go<HT, YT, XT, 1024, 2, VEC>(a, s);
+}
+template <typename HT, typename YT, typename XT>
+kdn_status bwd_vec(const BwdArgs& a, cudaStream_t s) {
+  return a.D % 8 == 0 ? bwd_size<HT, YT, XT, true>(a, s) : bwd_size<HT, YT, XT, false>(a, s);
 }
 template <typename HT, typename YT>
 kdn_status bwd_x(const BwdArgs& a, kdn_dtype x, cudaStream_t s) {
-  return x == KDN_F32 ? bwd_size<HT, YT, float>(a, s) : bwd_size<HT, YT, __nv_bfloat16>(a, s);
+  return x == KDN_F32 ? bwd_vec<HT, YT, float>(a, s) : bwd_vec<HT, YT, __nv_bfloat16>(a, s);
 }
 
 }  // namespace
@@ -328,10 +466,13 @@ kdn_status rmsnorm_forward_launch(const void* x, kdn_dtype xt, const void* res, 
                                   float* scale, int64_t rows, int D, float eps, cudaStream_t s) {
   const FwdArgs a{x, res, w, h, y, scale, rows, D, ldy, eps};
   using bf = __nv_bfloat16;
-  if (!res) rt = KDN_F32;  // not read
+  if (!res)  // (its type is not used)
+    return xt == KDN_F32 ? fwd_vec<float, float, false>(a, yt, s)
+                         : fwd_vec<bf, float, false>(a, yt, s);
   if (xt == KDN_F32)
-    return rt == KDN_F32 ? fwd_out<float, float>(a, yt, s) : fwd_out<float, bf>(a, yt, s);
-  return rt == KDN_F32 ? fwd_out<bf, float>(a, yt, s) : fwd_out<bf, bf>(a, yt, s);
+    return rt == KDN_F32 ? fwd_vec<float, float, true>(a, yt, s)
+                         : fwd_vec<float, bf, true>(a, yt, s);
+  return rt == KDN_F32 ? fwd_vec<bf, float, true>(a, yt, s) : fwd_vec<bf, bf, true>(a, yt, s);
 }
 
 kdn_status rmsnorm_backward_launch(const void* h, kdn_dtype ht, const float* w, const void* dy,
