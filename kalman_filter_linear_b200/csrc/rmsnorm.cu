@@ -11,9 +11,10 @@
 // One read of every input and one write of every output: a row stays in
 // registers between its reduction and its use, and the next row's loads are
 // under way meanwhile.  Rows are taken in turn by as many blocks as stay on the
-// device at once (one row a block of its own leaves each SM waiting at the
-// rows' starts and ends: 268 us in place of 90 for 32768 rows of 2048, fp32
-// in, e4m3 out).  A row has G threads.
+// device at once, eight elements a thread up to rows of 4096: 32768 rows of
+// 2048, fp32 with a bf16 stream to e4m3, take 90 us (6.7 TB/s), backward 128
+// (6.3 TB/s); a warp a row with 64 elements a lane, loaded as its turn came,
+// took 268 and 309.  A row has G threads.
 // VEC (rows of a multiple of 8): thread t holds the elements [8 (t + G v),
 // 8 (t + G v) + 8), so loads are 16 bytes a thread and a block of 128 is a half
 // warp's.  Otherwise rows do not start on 16-byte boundaries: a warp holds 256
@@ -71,14 +72,16 @@ __device__ __forceinline__ void put(T* row, int t, int vth, int D, const float (
   }
 }
 
-// Threads of a block, and the blocks of an SM that registers allow.
+// Threads of a block, rows of a block at once, and the blocks of an SM that
+// registers allow, forward and backward.
 template <int G, int NV, bool VEC>
 struct Shape {
-  static constexpr int THREADS = G < 256 ? 256 : G;
-  static constexpr int ROWS = THREADS / G;  // of a block at once
-  static constexpr int FWD = NV == 2 && VEC ? 512 : NV > 2 ? 512 : 1024;  // threads of an SM
-  static constexpr int BWD = G == 1024 ? 1024 : NV > 1 ? 512 : 768;
-  static constexpr int BLOCKS = FWD / THREADS, BWD_BLOCKS = BWD / THREADS;
+  enum : int {
+    THREADS = G < 256 ? 256 : G,
+    ROWS = THREADS / G,
+    BLOCKS = (NV > 2 || (NV == 2 && VEC) ? 512 : 1024) / THREADS,
+    BWD_BLOCKS = (G == 1024 ? 1024 : NV > 1 ? 512 : 768) / THREADS
+  };
 };
 
 // Sums over a row's G threads, in all of them.  Two buffers in turn: a slow
