@@ -38,8 +38,7 @@ constexpr int kLsWarps = 8;
 constexpr int kLsThreads = kLsWarps * 32;
 constexpr int kLsChannels = 64;  // channels of a tile
 constexpr int kLsFwdSteps = 8;   // steps of a warp, forward (16 spill)
-constexpr int kLsBwdSteps = 8;   // steps of a warp, backward
-constexpr int kLsShortestTile = 32;  // steps of the shortest tile of any kernel
+constexpr int kLsBwdSteps = 8;   // steps of a warp, backward (the workspace is sized by it)
 
 struct LsWs {
   uint32_t* error;    // device error word

@@ -221,9 +221,12 @@ kdn_status forward_types(const LsCall& k) {
 
 }  // namespace
 
-// of both directions and any types (more and shorter tiles need more)
+// Of both directions and any types.  Several entries (which are never packed)
+// of more than two columns always stream, and then need the error word alone.
 size_t linear_scan_workspace_size(int B, int T, int D) {
-  return ls_plan(B, T, D, kLsShortestTile).bytes;
+  const LsPlan p = ls_plan(B, T, D, kLsBwdSteps * kLsWarps);
+  const bool streams = B > 1 && p.cols > 2 && (int64_t)B * T < int64_t(1) << 33 && D < 1 << 27;
+  return streams ? 256 : p.bytes;
 }
 
 // B entries of T steps, or (cu) N sequences packed in T steps with B = 1

@@ -20,6 +20,8 @@
 // warp's.  Otherwise rows do not start on 16-byte boundaries: a warp holds 256
 // elements, lane l those at l, l + 32, ..., so that loads of single elements are
 // consecutive, and a block of 128 is a warp's.
+#include <atomic>
+
 #include "fp8_common.cuh"
 
 namespace kdn {
@@ -368,11 +370,16 @@ struct FwdArgs {
   float eps;
 };
 
+// blocks that the current device holds at once (0: an error)
 inline int64_t resident(int per_sm) {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  int sms = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (!sms) {
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
+  }
   return (int64_t)sms * per_sm;
 }
 

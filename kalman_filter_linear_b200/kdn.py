@@ -10,6 +10,7 @@ Function names match the C entry points.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -556,17 +557,18 @@ def _arg(t, name, dtype, shape, dev):
     """The data pointer of a checked tensor (None for a missing one)."""
     if t is None:
         return None
+    if isinstance(t, torch.Tensor) and t.device == dev and t.dtype is dtype and \
+            t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f'{name} must be a CUDA tensor')
     if t.dtype != dtype:
         raise TypeError(f'{name} must be {dtype}, got {t.dtype}')
     if t.shape != shape:
         raise ValueError(f'{name} must have shape {tuple(shape)}, got {tuple(t.shape)}')
-    if not t.is_contiguous():
-        raise ValueError(f'{name} must be contiguous')
     if t.device != dev:
         raise ValueError(f'{name} must be on {dev}, got {t.device}')
-    return t.data_ptr()
+    raise ValueError(f'{name} must be contiguous')
 
 
 def _cuda_tensor(t, name, ndim):
@@ -579,11 +581,14 @@ def _cuda_tensor(t, name, ndim):
 
 
 def _call(fn, dev, *args):
-    """Call an entry point with `dev` current, on its current stream."""
-    if torch.cuda.current_device() == dev.index:
-        return fn(*args, torch.cuda.current_stream().cuda_stream)
+    """Call an entry point with `dev` current, on its current stream.  (The two
+    torch._C calls are what torch.cuda.current_device and current_stream end in;
+    those cost 3 us a call, as much as the launch.)"""
+    index = dev.index
+    if torch._C._cuda_getDevice() == index:
+        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
     with torch.cuda.device(dev):
-        return fn(*args, torch.cuda.current_stream().cuda_stream)
+        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
 
 
 def _ws_arg(workspace, need, dev):
@@ -598,8 +603,29 @@ def _ws_arg(workspace, need, dev):
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
+@functools.lru_cache(maxsize=1024)
 def kdn_linear_scan_workspace_size(B, T, D):
     return int(lib().kdn_linear_scan_workspace_size(B, T, D))
+
+
+_status_words = {}
+
+
+def _scan_ws_arg(workspace, need, dev):
+    """_ws_arg; a call that needs no more than a status word, and whose caller
+    gave no place for one, shares the device's word that nobody reads."""
+    if workspace is None and 0 < need <= 256:
+        workspace = _status_words.get(dev)
+        if workspace is None:
+            workspace = _status_words[dev] = torch.empty(256, dtype=torch.uint8, device=dev)
+        return workspace, workspace.data_ptr(), 256
+    return _ws_arg(workspace, need, dev)
+
+
+def _f32_empty(like, shape, near):
+    """A new fp32 tensor, like the checked tensor `like` if there is one (which is
+    quicker), else on `near`'s device."""
+    return near.new_empty(shape, dtype=torch.float32) if like is None else torch.empty_like(like)
 
 
 def _scan_dims(a, cu_seqlens):
@@ -632,8 +658,8 @@ def kdn_linear_scan_forward(a, x, b=None, h0=None, cu_seqlens=None, y=None, h_ou
     if y is None:
         y = torch.empty_like(x)
     if h_out is None:
-        h_out = torch.empty(ends, dtype=f, device=dev)
-    workspace, pw, nw = _ws_arg(workspace, need, dev)
+        h_out = _f32_empty(h0, ends, a)
+    workspace, pw, nw = _scan_ws_arg(workspace, need, dev)
     st = _call(lib().kdn_linear_scan_forward, dev, pa, pb, gate, px, xt, p0, pc,
                _arg(y, 'y', x.dtype, shape, dev), _arg(h_out, 'h_out', f, ends, dev), B, T, D, pw,
                nw)
@@ -663,8 +689,8 @@ def kdn_linear_scan_backward(a, x, y, dy, b=None, h0=None, dh_T=None, cu_seqlens
     dx = torch.empty_like(y) if dx is None else dx
     if b is not None and db is None:
         db = torch.empty_like(b)
-    dh0 = torch.empty(ends, dtype=f, device=dev) if dh0 is None else dh0
-    workspace, pw, nw = _ws_arg(workspace, need, dev)
+    dh0 = _f32_empty(h0, ends, a) if dh0 is None else dh0
+    workspace, pw, nw = _scan_ws_arg(workspace, need, dev)
     st = _call(lib().kdn_linear_scan_backward, dev, pa, pb, gate, px, py, pdy, yt, p0, pT, pc,
                _arg(da, 'da', a.dtype, shape, dev),
                _arg(db, 'db', a.dtype, shape, dev) if b is not None else None,
@@ -693,10 +719,10 @@ def kdn_linear_scan_step(a, x, h, b=None, y=None):
     return y
 
 
-def _fp8_empty(rows, cols, dev):
-    """An e4m3 matrix whose rows start on 16-byte boundaries."""
+def _fp8_empty(rows, cols, near):
+    """An e4m3 matrix on `near`'s device whose rows start on 16-byte boundaries."""
     ld = (cols + 15) // 16 * 16
-    q = torch.empty((rows, ld), dtype=torch.float8_e4m3fn, device=dev)
+    q = near.new_empty((rows, ld), dtype=torch.float8_e4m3fn)
     return q if ld == cols else q[:, :cols]
 
 
@@ -744,15 +770,16 @@ def kdn_rmsnorm_forward(x, weight, residual=None, eps=1e-6, out_dtype=torch.bflo
         raise ValueError('h is an output only with a residual')
     ld, ps = 0, None
     if out_dtype == torch.float8_e4m3fn:
-        y = _fp8_empty(rows, D, dev) if y is None else y
+        y = _fp8_empty(rows, D, x) if y is None else y
         py, ld = _fp8_arg(y, 'y', rows, D, dev)
         blocks = (rows, (D + 127) // 128)
-        scale = torch.empty(blocks, dtype=torch.float32, device=dev) if scale is None else scale
+        scale = x.new_empty(blocks, dtype=torch.float32) if scale is None else scale
         ps = _arg(scale, 'scale', torch.float32, blocks, dev)
     else:
         if scale is not None:
             raise ValueError('scale is an output only for float8_e4m3fn')
-        y = torch.empty(x.shape, dtype=out_dtype, device=dev) if y is None else y
+        if y is None:
+            y = torch.empty_like(x) if out_dtype is x.dtype else x.new_empty(x.shape, dtype=out_dtype)
         py = _arg(y, 'y', out_dtype, x.shape, dev)
     if rows:
         st = _call(lib().kdn_rmsnorm_forward, dev, px, xt, pr, rt, pw, ph, py, _CODE[out_dtype],
@@ -761,6 +788,7 @@ def kdn_rmsnorm_forward(x, weight, residual=None, eps=1e-6, out_dtype=torch.bflo
     return y, scale, h
 
 
+@functools.lru_cache(maxsize=1024)
 def kdn_rmsnorm_backward_workspace_size(rows, D):
     return int(lib().kdn_rmsnorm_backward_workspace_size(rows, D))
 
@@ -784,10 +812,11 @@ def kdn_rmsnorm_backward(h, weight, dy, dh=None, eps=1e-6, x_dtype=None, want_re
     f, shape = torch.float32, h.shape
     ph, pw = _arg(h, 'h', h.dtype, shape, dev), _arg(weight, 'weight', f, (D,), dev)
     pdy, pdh = _arg(dy, 'dy', dy.dtype, shape, dev), _arg(dh, 'dh', h.dtype, shape, dev)
-    dx = torch.empty(shape, dtype=x_dtype, device=dev) if dx is None else dx
+    if dx is None:
+        dx = torch.empty_like(h) if x_dtype is h.dtype else h.new_empty(shape, dtype=x_dtype)
     if want_residual and dresidual is None:
-        dresidual = torch.empty(shape, dtype=h.dtype, device=dev)
-    dweight = torch.empty(D, dtype=f, device=dev) if dweight is None else dweight
+        dresidual = torch.empty_like(h)
+    dweight = torch.empty_like(weight) if dweight is None else dweight
     px, pr = _arg(dx, 'dx', x_dtype, shape, dev), _arg(dresidual, 'dresidual', h.dtype, shape, dev)
     pdw = _arg(dweight, 'dweight', f, (D,), dev)
     if rows == 0:
@@ -811,8 +840,8 @@ def kdn_fp8_quantize(x, tile=False, transpose=False, q=None, scale=None):
     px = _arg(x, 'x', x.dtype, x.shape, dev)
     R, C = (cols, rows) if transpose else (rows, cols)
     blocks = ((R + 127) // 128 if tile else R, (C + 127) // 128)
-    q = _fp8_empty(R, C, dev) if q is None else q
-    scale = torch.empty(blocks, dtype=torch.float32, device=dev) if scale is None else scale
+    q = _fp8_empty(R, C, x) if q is None else q
+    scale = x.new_empty(blocks, dtype=torch.float32) if scale is None else scale
     pq, ld = _fp8_arg(q, 'q', R, C, dev)
     ps = _arg(scale, 'scale', torch.float32, blocks, dev)
     if rows and cols:
@@ -843,7 +872,7 @@ def kdn_fp8_matmul(x, x_scale, w, w_scale, out_dtype=torch.bfloat16, out=None, s
         raise TypeError('x_scale must be a CUDA tensor')
     if out_dtype != torch.float32 and out_dtype != torch.bfloat16:
         raise TypeError(f'out_dtype must be bfloat16 or float32, got {out_dtype}')
-    out = torch.empty((M, N), dtype=out_dtype, device=dev) if out is None else out
+    out = x.new_empty((M, N), dtype=out_dtype) if out is None else out
     po = _arg(out, 'out', out_dtype, (M, N), dev)
     pst = _arg(status, 'status', torch.int32, (1,), dev)
     if M:
