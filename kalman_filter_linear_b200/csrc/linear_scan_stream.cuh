@@ -763,25 +763,40 @@ kdn_status ls_stream_go(const void* a, const void* x, const void* y, const void*
       return KDN_ERR_CUDA;
   }
   p.lines8 = (int64_t)entries * T / 8 * 8;
-  // the SMs of a device, and its shared memory limit for this kernel set
-  static std::atomic<int> ready[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return KDN_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.blockDim = dim3(kLsStreamThreads);
+  cfg.dynamicSmemBytes = S::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  // Clusters of 1, 2, 4 and 8 CTAs that a device holds at once (of eight fewer
+  // than its SMs would give: they do not span its parts), asked for once.
   auto kernel = linear_scan_stream_kernel<BWD, GT, XT, HAS_B, PACKED, EIGHT>;
-  int sms = dev < 64 ? ready[dev].load(std::memory_order_relaxed) : 0;
-  if (!sms) {
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::SMEM) !=
-            cudaSuccess)
+  static std::atomic<int> known[64][4];
+  int dev = 0, room[4];
+  if (cudaGetDevice(&dev) != cudaSuccess) return KDN_ERR_CUDA;
+  for (int i = 0; i < 4; ++i) room[i] = dev < 64 ? known[dev][i].load(std::memory_order_acquire) : 0;
+  if (!room[0] || !room[1] || !room[2] || !room[3]) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::SMEM) !=
+        cudaSuccess)
       return KDN_ERR_CUDA;
-    if (dev < 64) ready[dev].store(sms, std::memory_order_relaxed);
+    for (int i = 0; i < 4; ++i) {
+      at[0].val.clusterDim.x = 1u << i;
+      cfg.gridDim = dim3(1u << i);
+      if (cudaOccupancyMaxActiveClusters(&room[i], kernel, &cfg) != cudaSuccess || room[i] < 1)
+        return KDN_ERR_CUDA;
+      if (dev < 64) known[dev][i].store(room[i], std::memory_order_release);
+    }
   }
   // Tiles that a CTA works through one after another, for each cluster size;
   // a wave of maps costs a little more the more CTAs it comes from.
   int C = 0, clusters = 0;
   int64_t least = 0;
-  for (int c = 1; c <= kLsCluster; c *= 2) {
-    const int64_t slots = (int64_t)sms * S::CTAS / c, k = p.cols < slots ? p.cols : slots;
+  for (int i = 0, c = 1; c <= kLsCluster; ++i, c *= 2) {
+    const int64_t k = p.cols < room[i] ? p.cols : room[i];
     const int64_t waves = (p.chunks + c - 1) / c;
     if (c > 1 && same && waves < 3) continue;
     const int64_t cost = (p.cols + k - 1) / k * waves * (16 + c);
@@ -791,17 +806,8 @@ kdn_status ls_stream_go(const void* a, const void* x, const void* y, const void*
       least = cost;
     }
   }
-  cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(clusters * C));
-  cfg.blockDim = dim3(kLsStreamThreads);
-  cfg.dynamicSmemBytes = S::SMEM;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = (unsigned)C;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], m[3], m[4], p) == cudaSuccess
              ? KDN_OK
              : KDN_ERR_CUDA;
