@@ -29,13 +29,56 @@ __device__ __forceinline__ float fp8_scale(float amax) {
 __device__ __forceinline__ float fp8_inverse(float amax) {
   return kE4m3Max / max_nan(amax, kAmaxFloor);
 }
-// four codes of v * inv, the first in the lowest byte
-__device__ __forceinline__ uint32_t fp8_pack4(float v0, float v1, float v2, float v3, float inv) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v0 * inv, v1 * inv), __NV_SATFINITE,
-                                               __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v2 * inv, v3 * inv), __NV_SATFINITE,
-                                               __NV_E4M3);
+// four codes, the first in the lowest byte
+__device__ __forceinline__ uint32_t fp8_pack4(float q0, float q1, float q2, float q3) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(q0, q1), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(q2, q3), __NV_SATFINITE, __NV_E4M3);
   return lo | (hi << 16);
+}
+
+// A code is the rounding of a quotient that itself carries a few fp32 roundings,
+// so near the middle between two codes it may be the other one.  The middle of
+// two normal codes has the bits 1000... below the third of the fraction;
+// fp8_near tells whether a quotient is within ULPS units in the last place of
+// it, and such a quotient is decided again in fp64.  (Below 2^-6, the smallest
+// normal code, the roundings are that much smaller than the distance of two
+// codes.)
+template <uint32_t ULPS>
+__device__ __forceinline__ uint32_t fp8_from_middle(float q) {
+  return __float_as_uint(q) * 4096u + ((ULPS - 0x80000u) << 12);
+}
+template <uint32_t ULPS>
+__device__ __forceinline__ bool fp8_near(uint32_t from_middle) {
+  return from_middle <= 2u * ULPS << 12;
+}
+// The float nearest to q on the side of its middle that the exact quotient is
+// on; over: the sign of the exact magnitude less the middle's.
+__device__ __forceinline__ float fp8_side(float q, double over) {
+  const uint32_t b = (__float_as_uint(q) & 0xfff00000u) | 0x80000u;
+  return __uint_as_float(over > 0.0 ? b + 1u : over < 0.0 ? b - 1u : b);
+}
+__device__ __forceinline__ double fp8_middle(float q) {
+  return (double)fabsf(__uint_as_float((__float_as_uint(q) & 0xfff00000u) | 0x80000u));
+}
+// v * inv, with the block's largest magnitude `top`: two roundings, at most two
+// units.  448 |v| and a middle times `top` are exact in fp64.  (EXACT is for fp32: the quotients of bf16 numbers,
+// of eight bits each, are in a middle or far from it.)
+template <bool EXACT, int N>
+__device__ __forceinline__ void fp8_quotients(const float (&v)[N], float inv, float top,
+                                              float (&q)[N]) {
+  uint32_t near = ~0u;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    q[i] = v[i] * inv;
+    if (EXACT) near = min(near, fp8_from_middle<2>(q[i]));
+  }
+  if (EXACT && fp8_near<2>(near)) {
+    const double m = (double)max_nan(top, kAmaxFloor);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (fp8_near<2>(fp8_from_middle<2>(q[i])))
+        q[i] = fp8_side(q[i], 448.0 * (double)fabsf(v[i]) - fp8_middle(q[i]) * m);
+  }
 }
 
 // Eight consecutive elements from `p`: `n` of them exist (the others read as

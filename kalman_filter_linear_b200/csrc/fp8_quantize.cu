@@ -42,10 +42,13 @@ fp8_rows_kernel(const XT* __restrict__ X, uint8_t* __restrict__ Q, float* __rest
   if (e < C) {
     // (a row of Q has room for whole 16-byte pieces)
     uint4 c;
-    c.x = fp8_pack4(v[0][0], v[0][1], v[0][2], v[0][3], inv);
-    c.y = fp8_pack4(v[0][4], v[0][5], v[0][6], v[0][7], inv);
-    c.z = fp8_pack4(v[1][0], v[1][1], v[1][2], v[1][3], inv);
-    c.w = fp8_pack4(v[1][4], v[1][5], v[1][6], v[1][7], inv);
+    float q[8];
+    fp8_quotients<sizeof(XT) == 4>(v[0], inv, m, q);
+    c.x = fp8_pack4(q[0], q[1], q[2], q[3]);
+    c.y = fp8_pack4(q[4], q[5], q[6], q[7]);
+    fp8_quotients<sizeof(XT) == 4>(v[1], inv, m, q);
+    c.z = fp8_pack4(q[0], q[1], q[2], q[3]);
+    c.w = fp8_pack4(q[4], q[5], q[6], q[7]);
     *reinterpret_cast<uint4*>(Q + row * ldq + e) = c;
   }
   if ((threadIdx.x & 7) == 0) S[row * kb + e / 128] = fp8_scale(m);
@@ -70,8 +73,10 @@ fp8_rows_any_kernel(const XT* __restrict__ X, uint8_t* __restrict__ Q, float* __
   const float inv = fp8_inverse(m);
   if (n > 0) {
     uint2 c;
-    c.x = fp8_pack4(v[0], v[1], v[2], v[3], inv);
-    c.y = fp8_pack4(v[4], v[5], v[6], v[7], inv);
+    float q[8];
+    fp8_quotients<sizeof(XT) == 4>(v, inv, m, q);
+    c.x = fp8_pack4(q[0], q[1], q[2], q[3]);
+    c.y = fp8_pack4(q[4], q[5], q[6], q[7]);
     *reinterpret_cast<uint2*>(Q + row * ldq + e) = c;
   }
   if ((threadIdx.x & 15) == 0) S[row * kb + e / 128] = fp8_scale(m);
@@ -124,6 +129,8 @@ fp8_tile_kernel(const XT* __restrict__ X, uint8_t* __restrict__ Q, float* __rest
     v[i].load(X + (in ? (r0 + i) * C + c0 : 0), in ? nc : 0, vec);
   }
   float inv[8];
+  __shared__ float most_of[128];  // columns' largest, without TILE
+  float all_top = 0.f;
   if constexpr (TILE) {
     float m = 0.f;
 #pragma unroll
@@ -138,6 +145,7 @@ fp8_tile_kernel(const XT* __restrict__ X, uint8_t* __restrict__ Q, float* __rest
 #pragma unroll
     for (int w = 1; w < 8; ++w) m = max_nan(m, top[0][w]);
     if (threadIdx.x == 0) S[TR ? cb * rblocks + rb : rb * cblocks + cb] = fp8_scale(m);
+    all_top = m;
     const float all = fp8_inverse(m);
 #pragma unroll
     for (int e = 0; e < 8; ++e) inv[e] = all;
@@ -160,6 +168,7 @@ fp8_tile_kernel(const XT* __restrict__ X, uint8_t* __restrict__ Q, float* __rest
       const int64_t c = cb * 128 + threadIdx.x;
       if (c < C) S[c * rblocks + rb] = fp8_scale(m);
       top[0][threadIdx.x] = fp8_inverse(m);  // (this thread alone uses the column)
+      most_of[threadIdx.x] = m;
     }
     __syncthreads();
 #pragma unroll
@@ -170,8 +179,12 @@ fp8_tile_kernel(const XT* __restrict__ X, uint8_t* __restrict__ Q, float* __rest
     for (int i = 0; i < 8; ++i) {
       if (r0 + i < R && nc > 0) {
         uint2 c;
-        c.x = fp8_pack4(v[i].at(0), v[i].at(1), v[i].at(2), v[i].at(3), inv[0]);
-        c.y = fp8_pack4(v[i].at(4), v[i].at(5), v[i].at(6), v[i].at(7), inv[0]);
+        float x[8], q[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = v[i].at(e);
+        fp8_quotients<sizeof(XT) == 4>(x, inv[0], all_top, q);
+        c.x = fp8_pack4(q[0], q[1], q[2], q[3]);
+        c.y = fp8_pack4(q[4], q[5], q[6], q[7]);
         *reinterpret_cast<uint2*>(Q + (r0 + i) * ldq + c0) = c;
       }
     }
@@ -180,8 +193,12 @@ fp8_tile_kernel(const XT* __restrict__ X, uint8_t* __restrict__ Q, float* __rest
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       uint2 c;
-      c.x = fp8_pack4(v[0].at(e), v[1].at(e), v[2].at(e), v[3].at(e), inv[e]);
-      c.y = fp8_pack4(v[4].at(e), v[5].at(e), v[6].at(e), v[7].at(e), inv[e]);
+      float x[8], q[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = v[i].at(e);
+      fp8_quotients<sizeof(XT) == 4>(x, inv[e], TILE ? all_top : most_of[cv * 8 + e], q);
+      c.x = fp8_pack4(q[0], q[1], q[2], q[3]);
+      c.y = fp8_pack4(q[4], q[5], q[6], q[7]);
       turned[cv * 8 + e][rr ^ cv] = c;
     }
     __syncthreads();

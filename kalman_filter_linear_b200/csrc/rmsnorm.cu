@@ -108,6 +108,50 @@ __device__ __forceinline__ void row_sums(float (&x)[N], float (*sh)[N], int turn
   }
 }
 
+// The quotients of a block's codes from y = h rs w and its largest magnitude
+// `top` (the block: N elements of each of LANES threads).  The factor rs is the
+// same in all of them, so a quotient is 448 h w / max |h w|; where the six
+// roundings of q (two each of y and top, one of the inverse and one of the
+// product: less than six units in the last place) could decide a code, the warp
+// decides it so, in fp64.  (One row of 2048 in forty has such a place.)
+template <int N, int LANES>
+__device__ __noinline__ void norm_decide(const float* h, const float* w, float* q) {
+  double most = 0.0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) most = fmax(most, fabs((double)h[i] * (double)w[i]));
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) most = fmax(most, __shfl_xor_sync(0xffffffffu, most, o));
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (fp8_near<6>(fp8_from_middle<6>(q[i])))
+      q[i] = fp8_side(q[i], 448.0 * fabs((double)h[i] * (double)w[i]) - fp8_middle(q[i]) * most);
+}
+template <int N, int LANES>
+__device__ __forceinline__ void norm_quotients(const float (&y)[N], const float (&h)[N],
+                                               const float (&w)[N], float top, float (&q)[N]) {
+  const float inv = fp8_inverse(top);
+  uint32_t near = ~0u;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    q[i] = y[i] * inv;
+    near = min(near, fp8_from_middle<6>(q[i]));
+  }
+  if (!__any_sync(0xffffffffu, fp8_near<6>(near))) return;
+  float a[N], b[N], c[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    a[i] = h[i];
+    b[i] = w[i];
+    c[i] = q[i];
+  }
+  norm_decide<N, LANES>(a, b, c);
+  // (a block below the floor, or one that is not finite, keeps what it has)
+  if (top > kAmaxFloor && top <= 3.0e38f) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) q[i] = c[i];
+  }
+}
+
 template <typename XT, typename RT, bool RES, Out OUT, int G, int NV, bool VEC>
 __global__ void __launch_bounds__(Shape<G, NV, VEC>::THREADS, Shape<G, NV, VEC>::BLOCKS)
 rmsnorm_forward_kernel(const XT* __restrict__ X, const RT* Res, const float* __restrict__ W,
@@ -172,42 +216,50 @@ rmsnorm_forward_kernel(const XT* __restrict__ X, const RT* Res, const float* __r
         hw.template load<G>(W, t, v, D);
         hw.get(w[v]);
       }
+      float y[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[v][i] = h[v][i] * rs * w[v][i];
+      for (int i = 0; i < 8; ++i) y[i] = h[v][i] * rs * w[v][i];
       if (OUT == Out::F32) {
-        if (have) put<G, VEC>(static_cast<float*>(Yv) + row * D, t, v, D, h[v]);
+        if (have) put<G, VEC>(static_cast<float*>(Yv) + row * D, t, v, D, y);
       } else if (OUT == Out::BF16) {
-        if (have) put<G, VEC>(static_cast<__nv_bfloat16*>(Yv) + row * D, t, v, D, h[v]);
+        if (have) put<G, VEC>(static_cast<__nv_bfloat16*>(Yv) + row * D, t, v, D, y);
       } else if constexpr (VEC) {
         // elements behind the row's end are zeros here: they do not raise the
         // maximum
         const int e = 8 * (t + G * v);
-        const float top = half_warp_max(amax8(h[v]));
-        const float inv = fp8_inverse(top);
+        const float top = half_warp_max(amax8(y));
+        float q[8];
+        norm_quotients<8, 16>(y, h[v], w[v], top, q);
         if (have && e < D) {
           uint2 c;
-          c.x = fp8_pack4(h[v][0], h[v][1], h[v][2], h[v][3], inv);
-          c.y = fp8_pack4(h[v][4], h[v][5], h[v][6], h[v][7], inv);
+          c.x = fp8_pack4(q[0], q[1], q[2], q[3]);
+          c.y = fp8_pack4(q[4], q[5], q[6], q[7]);
           *reinterpret_cast<uint2*>(static_cast<uint8_t*>(Yv) + row * ldy + e) = c;
           if ((t & 15) == 0) Scale[row * ((D + 127) / 128) + e / 128] = fp8_scale(top);
         }
       } else {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const float(&q)[8] = h[v];
           const int e = 256 * ((t >> 5) + G / 32 * v) + 128 * half + (t & 31);
-          float top = fabsf(q[4 * half]);
+          float z[4], hz[4], wz[4], q[4];
 #pragma unroll
-          for (int i = 1; i < 4; ++i) top = max_nan(top, fabsf(q[4 * half + i]));
+          for (int i = 0; i < 4; ++i) {
+            z[i] = y[4 * half + i];
+            hz[i] = h[v][4 * half + i];
+            wz[i] = w[v][4 * half + i];
+          }
+          float top = fabsf(z[0]);
+#pragma unroll
+          for (int i = 1; i < 4; ++i) top = max_nan(top, fabsf(z[i]));
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1)
             top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-          const uint32_t c = fp8_pack4(q[4 * half], q[4 * half + 1], q[4 * half + 2],
-                                       q[4 * half + 3], fp8_inverse(top));
-          uint8_t* y = static_cast<uint8_t*>(Yv) + row * ldy + e;
+          norm_quotients<4, 32>(z, hz, wz, top, q);
+          const uint32_t c = fp8_pack4(q[0], q[1], q[2], q[3]);
+          uint8_t* to = static_cast<uint8_t*>(Yv) + row * ldy + e;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (have && e + 32 * i < D) y[32 * i] = (uint8_t)(c >> (8 * i));
+            if (have && e + 32 * i < D) to[32 * i] = (uint8_t)(c >> (8 * i));
           if (have && (t & 31) == 0 && e < D)
             Scale[row * ((D + 127) / 128) + e / 128] = fp8_scale(top);
         }

@@ -94,6 +94,38 @@ def test_matmul(M, N, K, tile, out):
     assert (err <= tol + HALF[out] * (np.abs(want) + tol)).all(), (err - tol).max()
 
 
+@pytest.mark.parametrize("tile", [False, True])
+@pytest.mark.parametrize("out", [F32, BF16])
+@pytest.mark.parametrize("M,N,K", [(257, 1032, 130), (700, 1000, 1200), (2100, 2312, 260),
+                                   (513, 8, 384), (3000, 1544, 2050), (40, 4104, 640),
+                                   (64, 2056, 1100), (300, 120, 4300)])
+def test_matmul_tiles_that_end_early(M, N, K, out, tile):
+    """Pairs of blocks whose rows or columns end inside a tile, with outputs
+    that bulk copies store, sums over more blocks than scales come for at once,
+    and clusters that share a sum."""
+    x, sx = _codes(M, K, False, M)
+    w, sw = _codes(N, K, tile, N + 1)
+    got = kdn.kdn_fp8_matmul(x, sx, w, sw, out_dtype=out)
+    want, mag = fp8_ref.matmul(f64(x.float()), f64(sx), f64(w.float()), f64(sw), tile)
+    tol = (128 + 3 * -(-K // 128) + 8) * 2 * U * mag
+    tol = tol + HALF[out] * (np.abs(want) + tol)
+    assert (np.abs(f64(got) - want) <= tol).all()
+
+
+@pytest.mark.parametrize("tile", [False, True])
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("rows,cols", [(1500, 1024), (900, 1003)])
+def test_codes_of_fp32_are_the_exact_quotients(rows, cols, tile, transpose):
+    """Of a million numbers a few quotients lie so near the middle of two codes
+    that the roundings of fp32 would decide: the code is the exact quotient's.
+    (An fp64 quotient is within 2^-52, which no element here comes near to.)"""
+    x = _matrix(rows, cols, F32, seed=rows + 1)
+    q, _ = kdn.kdn_fp8_quantize(x, tile=tile, transpose=transpose)
+    v = f64(x).T if transpose else f64(x)
+    top = fp8_ref.spread(fp8_ref.scales(v, tile) * 448.0, *v.shape, tile)
+    assert (f64(q.float()) == fp8_ref.e4m3(448.0 * v / top)).all()
+
+
 def test_matmul_small_integers_are_exact():
     """Codes that are small integers with scales of one: every sum is an
     integer below 2^24, so the product has to be exact."""

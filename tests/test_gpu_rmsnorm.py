@@ -92,6 +92,20 @@ def test_backward(rows, D, ht, yt, xt, through):
     assert (np.abs(f64(g['weight']) - dw) <= (64 + rows / 592 + 74 + 16) * U * mw).all()
 
 
+@pytest.mark.parametrize("rows,D", [(700, 2048), (700, 1001), (150, 8200)])
+def test_codes_are_the_exact_quotients(rows, D):
+    """The factor of a row's norm is in all its elements alike, so a code is that
+    of 448 h w / max |h w| over its block, also where fp32 roundings would
+    decide between two."""
+    g = torch.Generator().manual_seed(rows + D)
+    x = torch.randn(rows, D, generator=g).cuda()
+    w = (1 + 0.1 * torch.randn(D, generator=g)).cuda()
+    y, _, _ = kdn.kdn_rmsnorm_forward(x, w, out_dtype=torch.float8_e4m3fn)
+    u = f64(x) * f64(w)
+    top = fp8_ref.spread(fp8_ref.scales(u) * 448.0, rows, D)
+    assert (f64(y.float()) == fp8_ref.e4m3(448.0 * u / top)).all()
+
+
 def test_rows_of_zeros_and_tiny_or_huge_values():
     D = 256
     x = torch.zeros(5, D, device='cuda')
