@@ -407,7 +407,7 @@ fp8_matmul_wide(const __grid_constant__ CUtensorMap mx, const __grid_constant__ 
       if constexpr (TILE) tmem_ld_async(from + 32 * (c & 1), r[c & 1]);
       else tmem_ld_rows16(from + ((uint32_t)(16 * (c & 1)) << 16), r[c & 1]);
     };
-    uint32_t it = 0, g = 0;
+    uint32_t g = 0, buf = 0, phase = 0;
     bool bad = false;
     for (int tile = pair; tile < tiles && !bad; tile += pairs) {
       const int mw0 = tile / tiles_n * 256 + (int)rank * 128 + 32 * q;
@@ -417,13 +417,15 @@ fp8_matmul_wide(const __grid_constant__ CUtensorMap mx, const __grid_constant__ 
       for (int c = 0; c < CHUNKS; ++c)
 #pragma unroll
         for (int j = 0; j < 16; ++j) acc[c][j] = make_float2(0.f, 0.f);
-      if (warp_fail(&tfull[it % BUFS], (it / BUFS) & 1u)) break;
+      if (warp_fail(&tfull[buf], phase)) break;
       tc_fence_after();
-      read(it % BUFS, 0);
-      for (int kb = 0; kb < p.kbs; ++kb, ++it) {
-        const int k = kb % kScaleBlocks;
-        if (k == 0 && warp_fail(&sc_full[g & 1u], (g >> 1) & 1u)) { bad = true; break; }
-        const float* sc = scales + (g & 1u) * (W::SC / 4) + k * W::SCV;
+      read(buf, 0);
+      const float* sc = nullptr;
+      for (int kb = 0, k = 0; kb < p.kbs; ++kb) {
+        if (k == 0) {
+          if (warp_fail(&sc_full[g & 1u], (g >> 1) & 1u)) { bad = true; break; }
+          sc = scales + (g & 1u) * (W::SC / 4);
+        }
         float s[TILE ? 1 : 4];
         if constexpr (TILE) {
           s[0] = sc[32 * q + lane] * sc[128 + (h * CW >> 7)];
@@ -432,8 +434,8 @@ fp8_matmul_wide(const __grid_constant__ CUtensorMap mx, const __grid_constant__ 
           for (int i = 0; i < 4; ++i) s[i] = sc[32 * q + gr + 8 * i];
         }
         const float* cs = sc + 128 + h * CW + gc;
-        const uint32_t buf = it % BUFS;
-        const uint32_t nbuf = (it + 1) % BUFS, nphase = (it + 1) / BUFS & 1u;
+        const uint32_t nbuf = buf + 1 == (uint32_t)BUFS ? 0 : buf + 1;
+        const uint32_t nphase = nbuf == 0 ? phase ^ 1u : phase;
         bool ready = false;  // the next block, asked for ahead
         float2 w[8];
 #pragma unroll
@@ -476,8 +478,12 @@ fp8_matmul_wide(const __grid_constant__ CUtensorMap mx, const __grid_constant__ 
           }
         }
         if (bad) break;
-        if (k == kScaleBlocks - 1 || kb == p.kbs - 1) {
+        buf = nbuf;
+        phase = nphase;
+        sc += W::SCV;
+        if (++k == kScaleBlocks || kb == p.kbs - 1) {
           // this warp has used the scales
+          k = 0;
           __syncwarp();
           if (lane == 0) mbar_arrive(&sc_empty[g & 1u]);
           ++g;
