@@ -78,9 +78,12 @@ struct LsStage {
   // bytes of a step and channel over all inputs
   static constexpr int G = sizeof(GT), X = sizeof(XT);
   static constexpr int PER = BWD ? G + 2 * X + (HAS_B ? G + X : 0) : G + X + (HAS_B ? G : 0);
-  // steps of a warp, so that a CTA of two an SM has three stages at least
+  // Steps of a warp, so that a CTA of two an SM has three stages at least.
+  // Without EIGHT a tile of 16 steps is mostly copies of two rows each, so there
+  // it is 32 steps, with one CTA an SM where that needs more room (8 x 6597 x 45,
+  // backward with fp32 gates: 47 us in place of 87; 8 x 4096 x 2047 434 and 444).
   static constexpr int WIDE = EIGHT ? 64 : 72;  // (at most)
-  static constexpr int LW = PER * WIDE * 64 <= 30000 ? 16 : PER * WIDE * 32 <= 30000 ? 8 : 4;
+  static constexpr int LW = PER * WIDE * 64 <= 30000 ? 16 : PER * WIDE * 32 <= 30000 || !EIGHT ? 8 : 4;
   static constexpr int STEPS = 4 * LW;
   // channels of a row as copied, and elements of a box: a tensor's whole tile,
   // or every eighth row of it (boxes start on 128 bytes)
@@ -104,7 +107,7 @@ struct LsStage {
   static constexpr __device__ int at_x(int i, uint32_t e) {
     return EIGHT ? i * WX : (i & 7) * BX + (i >> 3) * WX + (int)(e & (16 / X - 1));
   }
-  static constexpr int CTAS = 2;  // of an SM
+  static constexpr int CTAS = BYTES > 29400 ? 1 : 2;  // of an SM
   // (the static arrays take less than 26.5 KB, the system 1 KB a CTA)
   static constexpr int ROOM = (233472 / CTAS - 1024 - 27136 - 128) / (int)BYTES;
   static constexpr int STAGES = ROOM < 6 ? ROOM : 6;
@@ -127,19 +130,20 @@ __device__ __forceinline__ void ls_tma_load(void* dst, const void* tmap, uint64_
       "l"(tmap), "r"(smem_u32(bar)), "r"(c), "r"(t)
       : "memory");
 }
-// A tensor's tile from global row R, channel c0 (steps t of entry bi).  es:
-// bytes of an element; box: bytes of a box.
+// A tensor's tile from global row R, channel c0 (steps t of entry bi), by lane 0,
+// or each box by a lane of its own (a thread that issues all of a tile's 24 to
+// 40 copies holds the ring up: 8 x 6597 x 45, backward with fp32 gates, 98 us in place of
+// 87).
+// es: bytes of an element; box: bytes of a box.
 template <bool EIGHT>
 __device__ __forceinline__ void ls_copy(uint8_t* dst, const void* tmap, uint64_t* bar, int c0, int t,
-                                        int bi, int64_t R, int D, int es, uint32_t box) {
+                                        int bi, int64_t R, int D, int es, uint32_t box, int lane) {
   if constexpr (EIGHT) {
-    ls_tma_load(dst, tmap, bar, c0, t, bi);
-  } else {
-    for (int m = 0; m < 8; ++m) {
-      const int64_t row = R + m;
-      const int x = ((int)(row & 7) * D + c0) & ~(16 / es - 1);
-      ls_tma_load(dst + m * box, tmap, bar, x, (int)(row >> 3));
-    }
+    if (lane == 0) ls_tma_load(dst, tmap, bar, c0, t, bi);
+  } else if (lane < 8) {
+    const int64_t row = R + lane;
+    const int x = ((int)(row & 7) * D + c0) & ~(16 / es - 1);
+    ls_tma_load(dst + lane * box, tmap, bar, x, (int)(row >> 3));
   }
 }
 __device__ __forceinline__ float2 ls_sh2(const float* p) { return *reinterpret_cast<const float2*>(p); }
@@ -299,41 +303,43 @@ linear_scan_stream_kernel(const __grid_constant__ CUtensorMap ma, const __grid_c
 
   if (warp == 4 * G) {
     // ------------------------------------------------------------- copies
-    if (lane == 0) {
-      int64_t n = 0;
-      int st = 0;
-      uint32_t phase = 1;
-      Pos q{col0, 0};
-      for (; n < total; ++n, next(q, 1)) {
-        if (n >= NS && fail(&empty[st], phase)) break;
-        const int j = q.wave * C + rank;
-        if (j < p.chunks) {
-          const int bi = (int)(q.col / p.groups), t = tile_start(j);
-          const int c0 = (int)(q.col - (int64_t)bi * p.groups) * kLsChannels;
-          uint8_t* d = sm + (uint32_t)st * S::BYTES;
-          const int64_t R = (int64_t)bi * p.T + t;
-          mbar_expect_tx(&full[st], S::SENT);
-          auto copy = [&](uint32_t at, const CUtensorMap& m, int back, int es, uint32_t box) {
-            ls_copy<EIGHT>(d + at, &m, &full[st], c0, t - back, bi, R - back, p.D, es, box);
-          };
-          copy(S::A, ma, 0, S::G, S::BG * S::G);
-          copy(S::X0, mx, 0, S::X, S::BX * S::X);
-          if (BWD) copy(S::Y, my, 1, S::X, S::BX * S::X);
-          if (HAS_B) copy(S::B, mb, 0, S::G, S::BG * S::G);
-          if (BWD && HAS_B) copy(S::X1, mx1, 0, S::X, S::BX * S::X);
-        } else {
-          mbar_arrive(&full[st]);
-        }
-        if (++st == NS) {
-          st = 0;
-          phase ^= 1u;
-        }
+    int64_t n = 0;
+    int st = 0;
+    uint32_t phase = 1;
+    Pos q{col0, 0};
+    // (one lane where it issues alone: a vote of the warp each time costs 6 %)
+    for (; n < total && (!EIGHT || lane == 0); ++n, next(q, 1)) {
+      const bool bad = n >= NS && lane == 0 && fail(&empty[st], phase);
+      if (EIGHT ? bad : __any_sync(0xffffffffu, bad) != 0) break;
+      const int j = q.wave * C + rank;
+      if (j < p.chunks) {
+        const int bi = (int)(q.col / p.groups), t = tile_start(j);
+        const int c0 = (int)(q.col - (int64_t)bi * p.groups) * kLsChannels;
+        uint8_t* d = sm + (uint32_t)st * S::BYTES;
+        const int64_t R = (int64_t)bi * p.T + t;
+        if (lane == 0) mbar_expect_tx(&full[st], S::SENT);
+        if (!EIGHT) __syncwarp();
+        auto copy = [&](uint32_t at, const CUtensorMap& m, int back, int es, uint32_t box) {
+          ls_copy<EIGHT>(d + at, &m, &full[st], c0, t - back, bi, R - back, p.D, es, box, lane);
+        };
+        copy(S::A, ma, 0, S::G, S::BG * S::G);
+        copy(S::X0, mx, 0, S::X, S::BX * S::X);
+        if (BWD) copy(S::Y, my, 1, S::X, S::BX * S::X);
+        if (HAS_B) copy(S::B, mb, 0, S::G, S::BG * S::G);
+        if (BWD && HAS_B) copy(S::X1, mx1, 0, S::X, S::BX * S::X);
+      } else if (lane == 0) {
+        mbar_arrive(&full[st]);
       }
-      // copies in flight land before the CTA's memory goes, whatever became
-      // of the other warps (bounded)
+      if (++st == NS) {
+        st = 0;
+        phase ^= 1u;
+      }
+    }
+    // copies in flight land before the CTA's memory goes, whatever became of
+    // the other warps (bounded)
+    if (lane == 0)
       for (int64_t i = n > NS ? n - NS : 0; i < n; ++i)
         mbar_wait(&full[i % NS], (uint32_t)(i / NS) & 1u);
-    }
   } else if (warp == 4 * G + 1) {
     // --------------------------------------------------- the tile's map, sent
     Pos q{col0, 0};
