@@ -3,19 +3,24 @@
     python -m kalman_filter_linear_b200.build
 
 The library is a plain shared object with a C ABI (include/kdn.h); it links
-only the CUDA runtime.  Output: kalman_filter_linear_b200/libkdn.so.
+only the CUDA runtime.  Output: kalman_filter_linear_b200/libkdn.so, and beside it
+_kdn_quick.so, the quick form of the binding's small calls, which is built against
+torch's headers (without them the binding goes through ctypes alone).
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, 'libkdn.so')
+QUICK = os.path.join(PKG, '_kdn_quick.so')
 ARCH = ['-gencode', 'arch=compute_100a,code=sm_100a']
 
 
@@ -52,14 +57,39 @@ def build(verbose=False, extra=()):
         objs = list(ex.map(compile_one, srcs))
     subprocess.run([nvcc(), '-shared', *ARCH, '-o', LIB + '.tmp', *objs, '-lcudart'], check=True)
     os.replace(LIB + '.tmp', LIB)
+    build_quick(verbose)
     return LIB
+
+
+def build_quick(verbose=False):
+    """Compile _kdn_quick.so; without it the binding works the same, slower."""
+    spec = importlib.util.find_spec('torch')
+    cxx = shutil.which('g++')
+    if os.path.exists(QUICK):
+        os.remove(QUICK)
+    if spec is None or cxx is None:
+        return
+    torch = os.path.dirname(spec.origin)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    cmd = [cxx, '-O2', '-std=c++17', '-fPIC', '-shared', '-I', os.path.join(torch, 'include'),
+           '-I', os.path.join(torch, 'include', 'torch', 'csrc', 'api', 'include'),
+           '-I', os.path.join(cuda, 'include'), '-I', sysconfig.get_paths()['include'],
+           os.path.join(PKG, 'csrc', 'quick_binding.cpp'), '-o', QUICK + '.tmp', '-L', PKG,
+           '-l:libkdn.so', '-L', os.path.join(torch, 'lib'), '-lc10', '-lc10_cuda', '-ltorch',
+           '-ltorch_cpu', '-ltorch_python', '-Wl,-rpath,$ORIGIN']
+    if verbose:
+        print(' '.join(cmd), flush=True)
+    if subprocess.run(cmd).returncode == 0:
+        os.replace(QUICK + '.tmp', QUICK)
+    else:
+        print('_kdn_quick.so could not be built: calls go through ctypes', file=sys.stderr)
 
 
 def is_stale():
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(PKG, 'csrc', '*.cuh')) + \
+    deps = sources() + glob.glob(os.path.join(PKG, 'csrc', '*.cpp')) + glob.glob(os.path.join(PKG, 'csrc', '*.cuh')) + \
         glob.glob(os.path.join(PKG, 'csrc', '*.h')) + glob.glob(os.path.join(ROOT, 'include', '*.h'))
     return any(os.path.getmtime(d) > t for d in deps)
 

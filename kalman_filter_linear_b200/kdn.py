@@ -4,7 +4,9 @@ Argument marshalling only: every function checks that its tensors are CUDA
 (host, for kdn_forward_host), contiguous and of the right dtype, allocates
 outputs with PyTorch when the caller gives none, and passes raw pointers and
 the current CUDA stream to the C ABI.  All arithmetic happens in the library's kernels.  If
-``libkdn.so`` cannot be loaded the first call raises; there is no fallback.
+``libkdn.so`` cannot be loaded the first call raises; there is no fallback.  The
+calls around a layer (linear recurrence, norm, 8 bits), which are small when
+decoding, have a quick form in C++ that does the same (csrc/quick_binding.cpp).
 Function names match the C entry points.
 """
 from __future__ import annotations
@@ -547,6 +549,28 @@ def kdn_kla_forward(q, k, v, a, w, r, S0=None, lam0=None, o=None, S_out=None, la
 _CODE = {torch.float32: KDN_F32, torch.bfloat16: KDN_BF16, torch.float8_e4m3fn: KDN_E4M3}
 
 
+class _NoQuick:
+    """Stands in for a _kdn_quick.so that was not built."""
+    scan_step = scan_forward = scan_backward = norm_forward = norm_backward = quantize = matmul = \
+        staticmethod(lambda *args: None)
+
+
+_quick = None
+
+
+def _load_quick():
+    """The calls below in one C++ function each (csrc/quick_binding.cpp), which
+    gives None where anything is out of the ordinary; then the code here runs."""
+    global _quick
+    lib()
+    try:
+        from . import _kdn_quick
+        _quick = _kdn_quick
+    except ImportError:
+        _quick = _NoQuick
+    return _quick
+
+
 def _float_code(t, name):
     if t.dtype != torch.float32 and t.dtype != torch.bfloat16:
         raise TypeError(f'{name} must be bfloat16 or float32, got {t.dtype}')
@@ -646,6 +670,10 @@ def kdn_linear_scan_forward(a, x, b=None, h0=None, cu_seqlens=None, y=None, h_ou
     a and b share a dtype (fp32 or bf16), h0 [B, D] fp32.  Returns (y like x,
     h_T [B, D] fp32).  With cu_seqlens, the rows of y behind the last sequence
     are left as they were."""
+    if workspace is None:
+        r = (_quick or _load_quick()).scan_forward(a, x, b, h0, cu_seqlens, y, h_out)
+        if r is not None:
+            return r
     dev, B, T, D, need = _scan_dims(a, cu_seqlens)
     f, shape, ends = torch.float32, a.shape, (B, D)
     gate = _float_code(a, 'a')
@@ -672,6 +700,11 @@ def kdn_linear_scan_backward(a, x, y, dy, b=None, h0=None, dh_T=None, cu_seqlens
     """The gradients of kdn_linear_scan_forward, given its output y, dy like y
     and dh_T [B, D] fp32 (or None): a dict of a, x, h0 (fp32) and, when b is
     given, b.  x is read only with b, and may be None without."""
+    if workspace is None:
+        r = (_quick or _load_quick()).scan_backward(a, x, y, dy, b, h0, dh_T, cu_seqlens, da, dx, db,
+                                                    dh0)
+        if r is not None:
+            return r
     dev, B, T, D, need = _scan_dims(a, cu_seqlens)
     f, shape, ends = torch.float32, a.shape, (B, D)
     gate = _float_code(a, 'a')
@@ -706,6 +739,9 @@ def kdn_linear_scan_backward(a, x, y, dy, b=None, h0=None, dh_T=None, cu_seqlens
 def kdn_linear_scan_step(a, x, h, b=None, y=None):
     """One step of the recurrence: a, b, x [B, D], h [B, D] fp32 updated in
     place.  Returns y like x."""
+    r = (_quick or _load_quick()).scan_step(a, x, h, b, y)
+    if r is not None:
+        return r
     dev = _cuda_tensor(a, 'a', (2,))
     shape = a.shape
     gate, xt = _float_code(a, 'a'), _float_code(x, 'x')
@@ -751,6 +787,10 @@ def kdn_rmsnorm_forward(x, weight, residual=None, eps=1e-6, out_dtype=torch.bflo
     [rows, ceil(D / 128)] for e4m3 else None, and h = x + residual in the
     residual's dtype (None without a residual).  An e4m3 y is two-dimensional,
     its rows on 16-byte boundaries."""
+    r = (_quick or _load_quick()).norm_forward(x, weight, residual, eps, _CODE.get(out_dtype, -1), y,
+                                               scale, h)
+    if r is not None:
+        return r
     dev = _cuda_tensor(x, 'x', range(1, 9))
     D = x.shape[-1]
     rows = x.numel() // D if D else 0
@@ -800,6 +840,14 @@ def kdn_rmsnorm_backward(h, weight, dy, dh=None, eps=1e-6, x_dtype=None, want_re
     other use (h's dtype, or None).  Returns a dict of x (in x_dtype, h's by
     default), weight (fp32) and residual (h's dtype; by default when dh is
     given, else None)."""
+    if workspace is None:
+        want = dresidual is not None or (dh is not None if want_residual is None
+                                         else bool(want_residual))
+        r = (_quick or _load_quick()).norm_backward(
+            h, weight, dy, dh, eps, -1 if x_dtype is None else _CODE.get(x_dtype, 9), want, dx,
+            dresidual, dweight)
+        if r is not None:
+            return r
     dev = _cuda_tensor(h, 'h', range(1, 9))
     D = h.shape[-1]
     rows = h.numel() // D if D else 0
@@ -834,6 +882,9 @@ def kdn_fp8_quantize(x, tile=False, transpose=False, q=None, scale=None):
     each 128 of an output row, or with tile=True for each 128 x 128 tile;
     transpose=True quantises x's transpose.  Returns (q [R, C], its rows on
     16-byte boundaries; scale [R or ceil(R / 128), ceil(C / 128)])."""
+    r = (_quick or _load_quick()).quantize(x, tile, transpose, q, scale)
+    if r is not None:
+        return r
     dev = _cuda_tensor(x, 'x', (2,))
     rows, cols = x.shape
     xt = _float_code(x, 'x')
@@ -857,6 +908,9 @@ def kdn_fp8_matmul(x, x_scale, w, w_scale, out_dtype=torch.bfloat16, out=None, s
     [M, ceil(K / 128)], w_scale [ceil(N / 128), ceil(K / 128)] (128 x 128
     tiles) or [N, ceil(K / 128)], fp32.  Returns [M, N] in out_dtype (bfloat16
     or float32).  status: one zeroed int32 word that a timed-out wait sets."""
+    r = (_quick or _load_quick()).matmul(x, x_scale, w, w_scale, _CODE.get(out_dtype, -1), out, status)
+    if r is not None:
+        return r
     dev = _cuda_tensor(x, 'x', (2,))
     _cuda_tensor(w, 'w', (2,))
     M, K = x.shape
