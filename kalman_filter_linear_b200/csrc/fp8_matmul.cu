@@ -9,18 +9,27 @@
 //
 // fp8_matmul_wide: 256 x BN outputs a tile, by the CTAs of a pair: each has 128
 // rows of x and half of w's rows in its shared memory, and one MMA
-// (cta_group::2) runs on both.  (A 128 x 256 tile of one CTA needs half as much
-// again from L2, which was its bound: 10.6 TB/s, whatever else was left out.)
+// (cta_group::2) runs on both, which loads a third less than tiles of one CTA
+// (128 x 256 each took 139 us for 32768 x 2048 x 2048, the pairs 132).
 // A CTA's warp 0 copies (TMA, 128-byte swizzle), warp 1 of the pair's first CTA
 // issues the MMAs, warps 2 and 3 bring the scales, eight blocks at a time and
 // turned so that a block's scales are consecutive, warps 4-11 scale and add:
 // four warps cover the 128 rows (TMEM lanes), each group half the columns.
 // Scaled sums leave through shared memory in bulk copies.
 //
+// 32768 x 2048 x 2048 takes 130 us (2.1 PFLOP/s), 2048 x 2048 x 32749 with a
+// scale for each row of w 200.  The loop without scaling takes 87 us, at the 1.25
+// to 1.4 GHz that the power limit leaves; with the hand-over of TMEM 96, with
+// its reads still 96, with the multiply-adds 125: a warp's own chain of read,
+// scale, add and release bounds it.  Handing TMEM over in parts of 128 columns
+// (145), sixteen scaling warps (143) and 128-column tiles with four accumulators
+// (152) were no faster.
+//
 // fp8_matmul_few: for few rows of x the bytes of w are what counts.  w is the
 // 128-row operand and up to 64 rows of x are the columns; the blocks of k are
 // split over a cluster of up to eight CTAs so that every SM streams w, and the
-// parts meet through distributed shared memory, added in rank order.
+// parts meet through distributed shared memory, added in rank order.  8 x 2048 x
+// 2048 takes 5.6 us, 8 x 8192 x 8192 12.6 (5.3 TB/s).
 //
 // Every wait is bounded; one that gives up sets the status word.
 #include <cuda.h>

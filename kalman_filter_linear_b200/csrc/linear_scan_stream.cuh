@@ -12,7 +12,9 @@
 // does not depend on timing.  (A look-back through global memory, in place of
 // the cluster, took 231 us for 8 x 4096 x 2048 with fp32 gates and 1034 us for
 // 65536 x 2048: a tile held its shared memory for the three to five L2 round
-// trips that a look-back takes.)
+// trips that a look-back takes.)  These take 85 and 183 us (6.3 and 5.9 TB/s),
+// the packed backward pass over 32768 x 2048 with fp32 gates 262 (6.1 TB/s):
+// HBM bounds them.
 //
 // Warps of a CTA: one copies inputs (bulk tensor copies) into a ring of stages;
 // two groups of four take the waves in turn, each warp a quarter of the tile's
@@ -29,6 +31,7 @@
 // wave n - 2, which took all maps of wave n - 2, and so every CTA had composed
 // wave n - 2 by then and finished wave n - 4, whose slot is the one to
 // overwrite.
+//
 // Rows of a multiple of 8 channels (EIGHT) are copied by their three
 // coordinates, 64 channels x the tile's steps at once, and a lane has the
 // channels 2 l and 2 l + 1.  Other rows do not start on the 16-byte boundaries
@@ -36,8 +39,10 @@
 // one matrix of eight rows a line, and a tile's rows of one remainder mod 8 are
 // a box of it, from the 16-byte boundary at or before their first channel.  So
 // a tile takes eight copies a tensor, its rows have a piece of 16 bytes more in
-// shared memory, and a lane has the channels l and l + 32.  The last rows, if
-// not a whole line, are in no box; the warps fetch them.
+// shared memory, and a lane has the channels l and l + 32.  (Keeping pairs of
+// channels where rows have an even length, with half the loads and stores,
+// gained 1 % at 3 x 37651 x 494.)  The last rows, if not a whole line, are in no
+// box; the warps fetch them.
 #pragma once
 
 #include <cuda.h>
