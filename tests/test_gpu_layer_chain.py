@@ -104,3 +104,40 @@ def test_norm_projections_and_linear_recurrence():
     want = linear_scan_ref.backward(f64(a[0]), f64(u[0]), f64(y[0]), f64(gn['x']), f64(b[0]))
     for name, ref in zip(('a', 'x', 'b', 'h0'), want):
         assert rel_maxabs(gs[name][0], ref) <= (OUT_TOL if name == 'x' else 1e-4), name
+
+
+def test_different_calls_on_many_streams_at_once():
+    """Products on pairs and on clusters, scans, norms and a mixing layer share
+    the SMs, their tensor memory and one status word, and give the bits that
+    each gives alone."""
+    from kalman_filter_linear_b200 import synth
+    g = torch.Generator().manual_seed(9)
+    t = lambda *s: torch.randn(*s, generator=g).cuda()
+    x8, sx = kdn.kdn_fp8_quantize(t(2048, 1024))
+    w8, sw = kdn.kdn_fp8_quantize(t(2048, 1024), tile=True)
+    v8, sv = kdn.kdn_fp8_quantize(t(1003, 1024))
+    a, u, h0 = torch.rand(2, 3000, 512, device='cuda'), t(2, 3000, 512), t(2, 512)
+    rows, w_norm = t(3000, 2048), t(2048)
+    q = {k: v.cuda() for k, v in synth.layer_inputs(2, 512, 4, 128, 128, 'iso', seed=0,
+                                                    dtype='bf16').items()}
+    calls = [lambda: kdn.kdn_fp8_matmul(x8, sx, w8, sw),
+             lambda: kdn.kdn_fp8_matmul(x8[:700], sx[:700], v8, sv, out_dtype=torch.float32),
+             lambda: kdn.kdn_fp8_matmul(x8[:40], sx[:40], w8, sw),
+             lambda: kdn.kdn_fp8_matmul(x8[:8], sx[:8], w8, sw),
+             lambda: kdn.kdn_linear_scan_forward(a, u, h0=h0)[0],
+             lambda: kdn.kdn_linear_scan_backward(a, None, u, u, h0=h0)['a'],
+             lambda: kdn.kdn_linear_scan_forward(a[:1, :, :64].contiguous(),
+                                                 u[:1, :, :64].contiguous())[1],
+             lambda: kdn.kdn_rmsnorm_forward(rows, w_norm, out_dtype=torch.float8_e4m3fn)[0].float(),
+             lambda: kdn.kdn_iso_forward(*(q[n] for n in 'qkvawr'))[0]]
+    want = [call() for call in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for turn in range(12):
+        got = []
+        for i, call in enumerate(calls):
+            with torch.cuda.stream(streams[(i + turn) % len(calls)]):
+                got.append(call())
+        torch.cuda.synchronize()
+        for i, (x, y) in enumerate(zip(got, want)):
+            assert torch.equal(x, y), (turn, i)
