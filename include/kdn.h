@@ -557,8 +557,8 @@ kdn_status kdn_linear_scan_step(const void* a, const void* b,
  * h        [rows, D] residual_dtype device output with a residual (may alias
  *          residual); NULL without
  * y        [rows, D] y_dtype device output; e4m3: rows ldy bytes apart, ldy a
- *          multiple of 16 and at least D (the bytes between D and the next
- *          multiple of 8 are overwritten).  ldy is not read otherwise.
+ *          multiple of 16 and at least D (the bytes behind D are left as they
+ *          were).  ldy is not read otherwise.
  * scale    [rows, ceil(D / 128)] fp32 device output, e4m3 only
  * eps      >= 0, finite
  * Sums in fp32: |h| up to about 1e18.  rows >= 0 (0: nothing is done);
@@ -615,7 +615,7 @@ kdn_status kdn_rmsnorm_backward(const void* h, kdn_dtype h_dtype,
  * q        e4m3 codes, device output: R rows of C bytes, ldq bytes apart, with
  *          (R, C) = (rows, cols), or (cols, rows) with transpose; ldq a
  *          multiple of 16 and at least C (the bytes between C and the next
- *          multiple of 16 may be overwritten)
+ *          multiple of 16 may be overwritten, but not behind the last row)
  * scale    [R, ceil(C / 128)] fp32 device output; with tile
  *          [ceil(R / 128), ceil(C / 128)]
  * rows >= 0 (0: nothing is done), cols >= 1; x and q 16-byte aligned.

@@ -21,12 +21,21 @@
 namespace kdn {
 namespace {
 
-template <typename XT>
-__global__ void __launch_bounds__(256)
-fp8_rows_kernel(const XT* __restrict__ X, uint8_t* __restrict__ Q, float* __restrict__ S,
-                int64_t rows, int C, int64_t ldq, int kb) {
+// Codes are stored in pieces of 8 or 16 bytes, into the room that a row of Q has
+// up to its next 16-byte boundary.  Behind the last row there need be no such
+// room.  Its end is always the last block's, which runs a copy of the code that
+// stores those codes one by one (LAST): the question asked in every block cost
+// 4 %.
+__device__ __forceinline__ void store_last(uint8_t* to, uint32_t lo, uint32_t hi, int n) {
+  for (int i = 0; i < n; ++i) to[i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
+}
+
+template <typename XT, bool LAST>
+__device__ __forceinline__ void rows_block(const XT* __restrict__ X, uint8_t* __restrict__ Q,
+                                           float* __restrict__ S, int64_t rows, int C, int64_t ldq,
+                                           int kb) {
   // unit: 16 elements of the row padded to whole blocks
-  const int64_t unit = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t unit = (int64_t)blockIdx.x * 128 + threadIdx.x;
   if (unit / 8 >= rows * kb) return;  // (whole groups of eight threads; no barrier below)
   const int64_t row = unit / (8 * kb);
   const int e = (int)(unit - row * 8 * kb) * 16;
@@ -40,7 +49,6 @@ fp8_rows_kernel(const XT* __restrict__ X, uint8_t* __restrict__ Q, float* __rest
   for (int o = 4; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(mask, m, o));
   const float inv = fp8_inverse(m);
   if (e < C) {
-    // (a row of Q has room for whole 16-byte pieces)
     uint4 c;
     float q[8];
     fp8_quotients<sizeof(XT) == 4>(v[0], inv, m, q);
@@ -49,15 +57,26 @@ fp8_rows_kernel(const XT* __restrict__ X, uint8_t* __restrict__ Q, float* __rest
     fp8_quotients<sizeof(XT) == 4>(v[1], inv, m, q);
     c.z = fp8_pack4(q[0], q[1], q[2], q[3]);
     c.w = fp8_pack4(q[4], q[5], q[6], q[7]);
-    *reinterpret_cast<uint4*>(Q + row * ldq + e) = c;
+    uint8_t* to = Q + row * ldq + e;
+    if (LAST && e + 16 > C && row + 1 == rows) *reinterpret_cast<uint2*>(to) = make_uint2(c.x, c.y);
+    else *reinterpret_cast<uint4*>(to) = c;
   }
   if ((threadIdx.x & 7) == 0) S[row * kb + e / 128] = fp8_scale(m);
 }
+// ENDS: rows end inside a piece.  (128 threads a block: with 256 fewer blocks are
+// under way when one ends.)
+template <typename XT, bool ENDS>
+__global__ void __launch_bounds__(128, 12)
+fp8_rows_kernel(const XT* __restrict__ X, uint8_t* __restrict__ Q, float* __restrict__ S,
+                int64_t rows, int C, int64_t ldq, int kb) {
+  if (!ENDS || blockIdx.x + 1 < gridDim.x) rows_block<XT, false>(X, Q, S, rows, C, ldq, kb);
+  else rows_block<XT, true>(X, Q, S, rows, C, ldq, kb);
+}
 
-template <typename XT>
-__global__ void __launch_bounds__(256)
-fp8_rows_any_kernel(const XT* __restrict__ X, uint8_t* __restrict__ Q, float* __restrict__ S,
-                    int64_t rows, int C, int64_t ldq, int kb) {
+template <typename XT, bool LAST>
+__device__ __forceinline__ void rows_any_block(const XT* __restrict__ X, uint8_t* __restrict__ Q,
+                                               float* __restrict__ S, int64_t rows, int C,
+                                               int64_t ldq, int kb) {
   // unit: 8 elements of the row padded to whole blocks
   const int64_t unit = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (unit / 16 >= rows * kb) return;  // (whole half warps; no barrier below)
@@ -77,9 +96,18 @@ fp8_rows_any_kernel(const XT* __restrict__ X, uint8_t* __restrict__ Q, float* __
     fp8_quotients<sizeof(XT) == 4>(v, inv, m, q);
     c.x = fp8_pack4(q[0], q[1], q[2], q[3]);
     c.y = fp8_pack4(q[4], q[5], q[6], q[7]);
-    *reinterpret_cast<uint2*>(Q + row * ldq + e) = c;
+    uint8_t* to = Q + row * ldq + e;
+    if (LAST && n < 8 && row + 1 == rows) store_last(to, c.x, c.y, n);
+    else *reinterpret_cast<uint2*>(to) = c;
   }
   if ((threadIdx.x & 15) == 0) S[row * kb + e / 128] = fp8_scale(m);
+}
+template <typename XT>
+__global__ void __launch_bounds__(256)
+fp8_rows_any_kernel(const XT* __restrict__ X, uint8_t* __restrict__ Q, float* __restrict__ S,
+                    int64_t rows, int C, int64_t ldq, int kb) {
+  if (blockIdx.x + 1 < gridDim.x) rows_any_block<XT, false>(X, Q, S, rows, C, ldq, kb);
+  else rows_any_block<XT, true>(X, Q, S, rows, C, ldq, kb);
 }
 
 // A thread's eight elements of a row, as they were loaded: bf16 pairs stay
@@ -113,11 +141,19 @@ struct Eight<__nv_bfloat16> {
 
 // TILE: one scale a tile, else one for each 128 along the output's rows.
 // (TR = false is only used with TILE.)
-template <typename XT, bool TILE, bool TR>
-__global__ void __launch_bounds__(256, sizeof(XT) == 2 ? 3 : 2)
-fp8_tile_kernel(const XT* __restrict__ X, uint8_t* __restrict__ Q, float* __restrict__ S,
-                int64_t R, int64_t C, int64_t ldq, int64_t rblocks, int64_t cblocks, int vec) {
-  __shared__ __align__(16) float top[16][128];
+template <bool TILE, bool TR>
+struct TileShared {
+  alignas(16) float top[TILE ? 1 : 16][128];
+  float most_of[TILE ? 1 : 128];  // columns' largest
+  uint2 turned[TR ? 128 : 1][16];
+};
+template <typename XT, bool TILE, bool TR, bool LAST>
+__device__ __forceinline__ void tile_block(TileShared<TILE, TR>& sh, const XT* __restrict__ X,
+                                           uint8_t* __restrict__ Q, float* __restrict__ S,
+                                           int64_t R, int64_t C, int64_t ldq, int64_t rblocks,
+                                           int64_t cblocks, int vec) {
+  auto& top = sh.top;
+  auto& most_of = sh.most_of;
   const int rr = threadIdx.x >> 4, cv = threadIdx.x & 15;
   const int64_t rb = blockIdx.x / cblocks, cb = blockIdx.x - rb * cblocks;
   const int64_t r0 = rb * 128 + rr * 8, c0 = cb * 128 + cv * 8;
@@ -129,7 +165,6 @@ fp8_tile_kernel(const XT* __restrict__ X, uint8_t* __restrict__ Q, float* __rest
     v[i].load(X + (in ? (r0 + i) * C + c0 : 0), in ? nc : 0, vec);
   }
   float inv[8];
-  __shared__ float most_of[128];  // columns' largest, without TILE
   float all_top = 0.f;
   if constexpr (TILE) {
     float m = 0.f;
@@ -185,11 +220,13 @@ fp8_tile_kernel(const XT* __restrict__ X, uint8_t* __restrict__ Q, float* __rest
         fp8_quotients<sizeof(XT) == 4>(x, inv[0], all_top, q);
         c.x = fp8_pack4(q[0], q[1], q[2], q[3]);
         c.y = fp8_pack4(q[4], q[5], q[6], q[7]);
-        *reinterpret_cast<uint2*>(Q + (r0 + i) * ldq + c0) = c;
+        uint8_t* to = Q + (r0 + i) * ldq + c0;
+        if (LAST && nc < 8 && r0 + i + 1 == R) store_last(to, c.x, c.y, nc);
+        else *reinterpret_cast<uint2*>(to) = c;
       }
     }
   } else {
-    __shared__ uint2 turned[128][16];
+    auto& turned = sh.turned;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       uint2 c;
@@ -207,13 +244,29 @@ fp8_tile_kernel(const XT* __restrict__ X, uint8_t* __restrict__ Q, float* __rest
       const int unit = k * 256 + threadIdx.x;
       const int c = unit >> 3, part = (unit & 7) * 2, x = c >> 3;
       const int64_t oc = cb * 128 + c, orow = rb * 128 + part * 8;
-      // (a row of Q has room for whole 16-byte pieces)
       if (oc < C && orow < R) {
         const uint2 a = turned[c][part ^ x], b = turned[c][(part + 1) ^ x];
-        *reinterpret_cast<uint4*>(Q + oc * ldq + orow) = make_uint4(a.x, a.y, b.x, b.y);
+        uint8_t* to = Q + oc * ldq + orow;
+        if (LAST && oc + 1 == C && orow + 16 > R) {
+          const int n = (int)(R - orow);
+          store_last(to, a.x, a.y, min(8, n));
+          store_last(to + 8, b.x, b.y, n - 8);
+        } else {
+          *reinterpret_cast<uint4*>(to) = make_uint4(a.x, a.y, b.x, b.y);
+        }
       }
     }
   }
+}
+template <typename XT, bool TILE, bool TR>
+__global__ void __launch_bounds__(256, sizeof(XT) == 2 ? 3 : 2)
+fp8_tile_kernel(const XT* __restrict__ X, uint8_t* __restrict__ Q, float* __restrict__ S,
+                int64_t R, int64_t C, int64_t ldq, int64_t rblocks, int64_t cblocks, int vec) {
+  __shared__ TileShared<TILE, TR> sh;
+  if (blockIdx.x + 1 < gridDim.x)
+    tile_block<XT, TILE, TR, false>(sh, X, Q, S, R, C, ldq, rblocks, cblocks, vec);
+  else
+    tile_block<XT, TILE, TR, true>(sh, X, Q, S, R, C, ldq, rblocks, cblocks, vec);
 }
 
 template <typename XT>
@@ -223,9 +276,12 @@ kdn_status quantize_types(const void* x, void* q, float* scale, int64_t R, int64
   uint8_t* Q = static_cast<uint8_t*>(q);
   const int64_t rb = (R + 127) / 128, cb = (C + 127) / 128;
   const int vec = C % 8 == 0;
-  if (!tile && !tr && vec)
-    fp8_rows_kernel<XT><<<(unsigned)((R * cb * 8 + 255) / 256), 256, 0, s>>>(X, Q, scale, R, (int)C,
-                                                                             ldq, (int)cb);
+  if (!tile && !tr && C % 16 == 0)
+    fp8_rows_kernel<XT, false><<<(unsigned)((R * cb * 8 + 127) / 128), 128, 0, s>>>(
+        X, Q, scale, R, (int)C, ldq, (int)cb);
+  else if (!tile && !tr && vec)
+    fp8_rows_kernel<XT, true><<<(unsigned)((R * cb * 8 + 127) / 128), 128, 0, s>>>(
+        X, Q, scale, R, (int)C, ldq, (int)cb);
   else if (!tile && !tr)
     fp8_rows_any_kernel<XT><<<(unsigned)((R * cb * 16 + 255) / 256), 256, 0, s>>>(
         X, Q, scale, R, (int)C, ldq, (int)cb);

@@ -881,7 +881,9 @@ def kdn_fp8_quantize(x, tile=False, transpose=False, q=None, scale=None):
     """x [rows, cols] (bfloat16 or float32) in e4m3 with fp32 scales: one for
     each 128 of an output row, or with tile=True for each 128 x 128 tile;
     transpose=True quantises x's transpose.  Returns (q [R, C], its rows on
-    16-byte boundaries; scale [R or ceil(R / 128), ceil(C / 128)])."""
+    16-byte boundaries; scale [R or ceil(R / 128), ceil(C / 128)]).  In a given q
+    the bytes between a row's end and the next multiple of 16 are overwritten,
+    but nothing behind the last row."""
     r = (_quick or _load_quick()).quantize(x, tile, transpose, q, scale)
     if r is not None:
         return r

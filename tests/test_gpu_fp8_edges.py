@@ -1,0 +1,65 @@
+"""Where the 8-bit calls end: outputs that the caller lays out to the last byte,
+empty batches, quotients next to the middle of two codes (needs a B200)."""
+import numpy as np
+import pytest
+import torch
+
+from kalman_filter_linear_b200 import kdn
+from oracle import fp8_ref
+from gpu_util import f64
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16, E4M3 = torch.float32, torch.bfloat16, torch.float8_e4m3fn
+GUARD = 0x55
+
+
+@pytest.fixture(params=['quick', 'python'])
+def form(request, monkeypatch):
+    """Both forms of the binding."""
+    if request.param == 'python':
+        monkeypatch.setattr(kdn, '_quick', kdn._NoQuick)
+
+
+def _guarded(R, C, more=0):
+    """An e4m3 matrix [R, C] whose last row ends at C, in a room of guard bytes;
+    which of the room's bytes lie between a row's end and the next multiple of
+    16, and which others are not the matrix's.  (One row is contiguous, whatever
+    its length.)"""
+    up = -(-C // 16) * 16
+    ld = up + more
+    room = torch.full((R * ld + 64,), GUARD, dtype=torch.uint8, device='cuda')
+    gaps, outside = torch.zeros_like(room, dtype=torch.bool), torch.ones_like(room, dtype=torch.bool)
+    for r in range(R):
+        outside[r * ld:r * ld + (up if r + 1 < R else C)] = False
+        gaps[r * ld + C:r * ld + up] = r + 1 < R
+    return room.view(E4M3).as_strided((R, C), (ld if R > 1 else C, 1)), room, gaps, outside
+
+
+@pytest.mark.parametrize("R,C", [(1, 1), (1, 7), (1, 8), (1, 100), (1, 104), (1, 112), (1, 131),
+                                 (3, 100), (130, 104), (20, 131), (20, 136), (129, 255)])
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("tile", [False, True])
+@pytest.mark.parametrize("transpose", [False, True])
+def test_quantize_writes_nothing_behind_a_given_matrix(R, C, dt, tile, transpose, form):
+    g = torch.Generator().manual_seed(R + C)
+    x = torch.randn(*((C, R) if transpose else (R, C)), generator=g).to(dt).cuda()
+    want, s_want = kdn.kdn_fp8_quantize(x, tile=tile, transpose=transpose)
+    for more in (0, 32):
+        q, room, _, outside = _guarded(R, C, more)
+        got, s = kdn.kdn_fp8_quantize(x, tile=tile, transpose=transpose, q=q)
+        assert got is q and torch.equal(s, s_want)
+        assert torch.equal(q.float(), want.float())
+        assert bool((room[outside] == GUARD).all())
+
+
+@pytest.mark.parametrize("R,C", [(1, 1), (1, 100), (1, 104), (3, 100), (40, 2056), (40, 1003)])
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_norm_writes_nothing_behind_a_row(R, C, dt, form):
+    g = torch.Generator().manual_seed(R + C)
+    x, w = torch.randn(R, C, generator=g).to(dt).cuda(), torch.rand(C, generator=g).cuda()
+    want, s_want, _ = kdn.kdn_rmsnorm_forward(x, w, out_dtype=E4M3)
+    y, room, gaps, outside = _guarded(R, C)
+    got, s, _ = kdn.kdn_rmsnorm_forward(x, w, out_dtype=E4M3, y=y)
+    assert got is y and torch.equal(s, s_want) and torch.equal(y.float(), want.float())
+    assert bool((room[outside | gaps] == GUARD).all())
