@@ -604,8 +604,7 @@ kdn_status kdn_rmsnorm_backward(const void* h, kdn_dtype h_dtype,
  * kdn_fp8_quantize -- a matrix into e4m3 codes with fp32 scales:
  *     scale = max(largest magnitude of the block, 2^-100) / 448
  *     code  = e4m3(value / scale), to nearest, ties to even
- * (of fp32 values the code of the exact quotient 448 value / magnitude; bf16
- * ones carry two fp32 roundings, which decide exact ties only).
+ * of the exact quotient 448 value / magnitude.
  * A block is 128 values along a row of the output (the last one may be
  * shorter), or with `tile` a 128 x 128 tile of it.  `transpose` quantises the
  * transpose of x.  An infinity or NaN in a block makes its scale infinite or

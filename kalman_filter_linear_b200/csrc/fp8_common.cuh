@@ -40,9 +40,7 @@ __device__ __forceinline__ uint32_t fp8_pack4(float q0, float q1, float q2, floa
 // so near the middle between two codes it may be the other one.  The middle of
 // two normal codes has the bits 1000... below the third of the fraction;
 // fp8_near tells whether a quotient is within ULPS units in the last place of
-// it, and such a quotient is decided again in fp64.  (Below 2^-6, the smallest
-// normal code, the roundings are that much smaller than the distance of two
-// codes.)
+// it, and such a quotient is decided again in fp64.
 template <uint32_t ULPS>
 __device__ __forceinline__ uint32_t fp8_from_middle(float q) {
   return __float_as_uint(q) * 4096u + ((ULPS - 0x80000u) << 12);
@@ -51,36 +49,71 @@ template <uint32_t ULPS>
 __device__ __forceinline__ bool fp8_near(uint32_t from_middle) {
   return from_middle <= 2u * ULPS << 12;
 }
+template <uint32_t ULPS, int N>
+__device__ __forceinline__ bool fp8_any_near(const float (&q)[N]) {
+  uint32_t near = ~0u;
+#pragma unroll
+  for (int i = 0; i < N; ++i) near = min(near, fp8_from_middle<ULPS>(q[i]));
+  return fp8_near<ULPS>(near);
+}
+// The middle of the two codes that q is between, as a float (it is one).
+__device__ __forceinline__ float fp8_middle(float q) {
+  return fabsf(__uint_as_float((__float_as_uint(q) & 0xfff00000u) | 0x80000u));
+}
 // The float nearest to q on the side of its middle that the exact quotient is
 // on; over: the sign of the exact magnitude less the middle's.
 __device__ __forceinline__ float fp8_side(float q, double over) {
-  const uint32_t b = (__float_as_uint(q) & 0xfff00000u) | 0x80000u;
-  return __uint_as_float(over > 0.0 ? b + 1u : over < 0.0 ? b - 1u : b);
+  const uint32_t b = __float_as_uint(fp8_middle(q));
+  return copysignf(__uint_as_float(over > 0.0 ? b + 1u : over < 0.0 ? b - 1u : b), q);
 }
-__device__ __forceinline__ double fp8_middle(float q) {
-  return (double)fabsf(__uint_as_float((__float_as_uint(q) & 0xfff00000u) | 0x80000u));
-}
-// v * inv, with the block's largest magnitude `top`: two roundings, at most two
-// units.  448 |v| and a middle times `top` are exact in fp64.  (EXACT is for fp32: the quotients of bf16 numbers,
-// of eight bits each, are in a middle or far from it.)
-template <bool EXACT, int N>
-__device__ __forceinline__ void fp8_quotients(const float (&v)[N], float inv, float top,
-                                              float (&q)[N]) {
-  uint32_t near = ~0u;
+// The quotients of a block's values, `top` its largest magnitude; and whether a
+// code has to be decided in fp64.
+// fp32: v * inv has two roundings, at most two units.
+// bf16: a quotient of two numbers of eight bits is the middle of two codes or
+// 2^-13 of itself away from it, and v hi + v lo, where hi + lo is the inverse to
+// more than twice the bits, rounds to the middle where it is one.
+template <typename XT>
+struct Fp8Block {
+  float inv, top;
+  __device__ __forceinline__ explicit Fp8Block(float m)
+      : inv(fp8_inverse(m)), top(max_nan(m, kAmaxFloor)) {}
+  // (through shared memory as two floats)
+  __device__ __forceinline__ Fp8Block(float a, float b) : inv(a), top(b) {}
+  __device__ __forceinline__ float first() const { return inv; }
+  __device__ __forceinline__ float second() const { return top; }
+  Fp8Block() = default;
+  template <int N>
+  __device__ __forceinline__ bool quotients(const float (&v)[N], float (&q)[N]) const {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    q[i] = v[i] * inv;
-    if (EXACT) near = min(near, fp8_from_middle<2>(q[i]));
+    for (int i = 0; i < N; ++i) q[i] = v[i] * inv;
+    return fp8_any_near<2>(q);
   }
-  if (EXACT && fp8_near<2>(near)) {
-    const double m = (double)max_nan(top, kAmaxFloor);
+};
+template <>
+struct Fp8Block<__nv_bfloat16> {
+  float hi, lo;
+  __device__ __forceinline__ explicit Fp8Block(float m) : hi(fp8_inverse(m)) {
+    const float top = max_nan(m, kAmaxFloor);
+    const float left = fmaf(-hi, top, kE4m3Max);  // exact
+    lo = top <= 3.4e38f ? left * hi * (1.f / kE4m3Max) : 0.f;
+  }
+  __device__ __forceinline__ Fp8Block(float a, float b) : hi(a), lo(b) {}
+  __device__ __forceinline__ float first() const { return hi; }
+  __device__ __forceinline__ float second() const { return lo; }
+  Fp8Block() = default;
+  template <int N>
+  __device__ __forceinline__ bool quotients(const float (&v)[N], float (&q)[N]) const {
+    const float2 h = make_float2(hi, hi), l = make_float2(lo, lo);
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (fp8_near<2>(fp8_from_middle<2>(q[i])))
-        q[i] = fp8_side(q[i], 448.0 * (double)fabsf(v[i]) - fp8_middle(q[i]) * m);
+    for (int i = 0; i < N; i += 2) {
+      const float2 x = make_float2(v[i], v[i + 1]);
+      const float2 r = __ffma2_rn(x, h, __fmul2_rn(x, l));
+      q[i] = r.x;
+      q[i + 1] = r.y;
+    }
+    return false;
   }
-}
-
+};
 // Eight consecutive elements from `p`: `n` of them exist (the others read as
 // 0).  vec: p is 16-byte aligned and all eight exist or none do.  On 32-byte
 // boundaries eight floats are one access: two of 16 bytes leave every other

@@ -21,6 +21,29 @@
 namespace kdn {
 namespace {
 
+// The codes of `n` values `step` apart, those near a middle decided in fp64: 448
+// |v| and a middle times `top` are exact there.  It reads the values again, so
+// that nothing but its arguments is kept for it: calls are rare, some three for a
+// million quotients (decided in place, 32768 x 2048 took 10 to 30 % longer).
+__device__ __noinline__ void fp8_codes_decided(const float* x, int64_t step, int n,
+                                               const Fp8Block<float> b, uint8_t* codes) {
+  for (int i0 = 0; i0 < n; i0 += 8) {
+    uint32_t which = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i0 + i < n && fp8_near<2>(fp8_from_middle<2>(x[(i0 + i) * step] * b.inv))) which |= 1u << i;
+    for (; which; which &= which - 1) {
+      const int i = i0 + __ffs(which) - 1;
+      const float v = x[i * step];
+      float q = v * b.inv;
+      q = fp8_side(q, 448.0 * (double)fabsf(v) - (double)fp8_middle(q) * (double)b.top);
+      codes[i] = (uint8_t)__nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
+    }
+  }
+}
+__device__ __forceinline__ void fp8_codes_decided(const __nv_bfloat16*, int64_t, int,
+                                                  const Fp8Block<__nv_bfloat16>&, uint8_t*) {}
+
 // Codes are stored in pieces of 8 or 16 bytes, into the room that a row of Q has
 // up to its next 16-byte boundary.  Behind the last row there need be no such
 // room.  Its end is always the last block's, which runs a copy of the code that
@@ -47,19 +70,20 @@ __device__ __forceinline__ void rows_block(const XT* __restrict__ X, uint8_t* __
   float m = max_nan(amax8(v[0]), amax8(v[1]));
 #pragma unroll
   for (int o = 4; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(mask, m, o));
-  const float inv = fp8_inverse(m);
+  const Fp8Block<XT> block(m);
   if (e < C) {
     uint4 c;
     float q[8];
-    fp8_quotients<sizeof(XT) == 4>(v[0], inv, m, q);
+    bool close = block.quotients(v[0], q);
     c.x = fp8_pack4(q[0], q[1], q[2], q[3]);
     c.y = fp8_pack4(q[4], q[5], q[6], q[7]);
-    fp8_quotients<sizeof(XT) == 4>(v[1], inv, m, q);
+    close |= block.quotients(v[1], q);
     c.z = fp8_pack4(q[0], q[1], q[2], q[3]);
     c.w = fp8_pack4(q[4], q[5], q[6], q[7]);
     uint8_t* to = Q + row * ldq + e;
     if (LAST && e + 16 > C && row + 1 == rows) *reinterpret_cast<uint2*>(to) = make_uint2(c.x, c.y);
     else *reinterpret_cast<uint4*>(to) = c;
+    if (close) fp8_codes_decided(x, 1, min(16, C - e), block, to);
   }
   if ((threadIdx.x & 7) == 0) S[row * kb + e / 128] = fp8_scale(m);
 }
@@ -89,16 +113,17 @@ __device__ __forceinline__ void rows_any_block(const XT* __restrict__ X, uint8_t
   float m = amax8(v);
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(mask, m, o));
-  const float inv = fp8_inverse(m);
+  const Fp8Block<XT> block(m);
   if (n > 0) {
     uint2 c;
     float q[8];
-    fp8_quotients<sizeof(XT) == 4>(v, inv, m, q);
+    const bool close = block.quotients(v, q);
     c.x = fp8_pack4(q[0], q[1], q[2], q[3]);
     c.y = fp8_pack4(q[4], q[5], q[6], q[7]);
     uint8_t* to = Q + row * ldq + e;
     if (LAST && n < 8 && row + 1 == rows) store_last(to, c.x, c.y, n);
     else *reinterpret_cast<uint2*>(to) = c;
+    if (close) fp8_codes_decided(X + row * C + e, 1, n, block, to);
   }
   if ((threadIdx.x & 15) == 0) S[row * kb + e / 128] = fp8_scale(m);
 }
@@ -139,21 +164,26 @@ struct Eight<__nv_bfloat16> {
   }
 };
 
+// The largest magnitudes of pairs of bf16 numbers: as integers they are in order,
+// NaN above infinity.
+__device__ __forceinline__ uint32_t max_pairs(uint32_t most, uint32_t a, uint32_t b) {
+  return __vimax3_u16x2(most, a & 0x7fff7fffu, b & 0x7fff7fffu);
+}
+
 // TILE: one scale a tile, else one for each 128 along the output's rows.
 // (TR = false is only used with TILE.)
-template <bool TILE, bool TR>
+template <typename XT, bool TILE, bool TR>
 struct TileShared {
   alignas(16) float top[TILE ? 1 : 16][128];
-  float most_of[TILE ? 1 : 128];  // columns' largest
+  alignas(16) float column[2][TILE ? 1 : 128];  // the columns' Fp8Blocks
   uint2 turned[TR ? 128 : 1][16];
 };
 template <typename XT, bool TILE, bool TR, bool LAST>
-__device__ __forceinline__ void tile_block(TileShared<TILE, TR>& sh, const XT* __restrict__ X,
+__device__ __forceinline__ void tile_block(TileShared<XT, TILE, TR>& sh, const XT* __restrict__ X,
                                            uint8_t* __restrict__ Q, float* __restrict__ S,
                                            int64_t R, int64_t C, int64_t ldq, int64_t rblocks,
                                            int64_t cblocks, int vec) {
   auto& top = sh.top;
-  auto& most_of = sh.most_of;
   const int rr = threadIdx.x >> 4, cv = threadIdx.x & 15;
   const int64_t rb = blockIdx.x / cblocks, cb = blockIdx.x - rb * cblocks;
   const int64_t r0 = rb * 128 + rr * 8, c0 = cb * 128 + cv * 8;
@@ -164,14 +194,22 @@ __device__ __forceinline__ void tile_block(TileShared<TILE, TR>& sh, const XT* _
     const bool in = r0 + i < R;
     v[i].load(X + (in ? (r0 + i) * C + c0 : 0), in ? nc : 0, vec);
   }
-  float inv[8];
-  float all_top = 0.f;
+  Fp8Block<XT> all;
   if constexpr (TILE) {
     float m = 0.f;
+    if constexpr (sizeof(XT) == 2 && !TR) {
+      uint32_t both = 0u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(v[i].at(e)));
+        for (int e = 0; e < 4; e += 2) both = max_pairs(both, v[i].w[e], v[i].w[e + 1]);
+      m = max_nan(__uint_as_float(both << 16), __uint_as_float(both & 0xffff0000u));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(v[i].at(e)));
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     if ((threadIdx.x & 31) == 0) top[0][threadIdx.x >> 5] = m;
@@ -180,18 +218,26 @@ __device__ __forceinline__ void tile_block(TileShared<TILE, TR>& sh, const XT* _
 #pragma unroll
     for (int w = 1; w < 8; ++w) m = max_nan(m, top[0][w]);
     if (threadIdx.x == 0) S[TR ? cb * rblocks + rb : rb * cblocks + cb] = fp8_scale(m);
-    all_top = m;
-    const float all = fp8_inverse(m);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) inv[e] = all;
+    all = Fp8Block<XT>(m);
   } else {
     // the largest of each column over the tile's 128 rows
     float most[8];
+    if constexpr (sizeof(XT) == 2) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      most[e] = fabsf(v[0].at(e));
+      for (int e = 0; e < 4; ++e) {
+        uint32_t both = 0u;
 #pragma unroll
-      for (int i = 1; i < 8; ++i) most[e] = max_nan(most[e], fabsf(v[i].at(e)));
+        for (int i = 0; i < 8; i += 2) both = max_pairs(both, v[i].w[e], v[i + 1].w[e]);
+        most[2 * e] = __uint_as_float(both << 16);
+        most[2 * e + 1] = __uint_as_float(both & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        most[e] = fabsf(v[0].at(e));
+#pragma unroll
+        for (int i = 1; i < 8; ++i) most[e] = max_nan(most[e], fabsf(v[i].at(e)));
+      }
     }
     reinterpret_cast<float4*>(&top[rr][cv * 8])[0] = make_float4(most[0], most[1], most[2], most[3]);
     reinterpret_cast<float4*>(&top[rr][cv * 8])[1] = make_float4(most[4], most[5], most[6], most[7]);
@@ -202,12 +248,11 @@ __device__ __forceinline__ void tile_block(TileShared<TILE, TR>& sh, const XT* _
       for (int k = 1; k < 16; ++k) m = max_nan(m, top[k][threadIdx.x]);
       const int64_t c = cb * 128 + threadIdx.x;
       if (c < C) S[c * rblocks + rb] = fp8_scale(m);
-      top[0][threadIdx.x] = fp8_inverse(m);  // (this thread alone uses the column)
-      most_of[threadIdx.x] = m;
+      const Fp8Block<XT> b(m);
+      sh.column[0][threadIdx.x] = b.first();
+      sh.column[1][threadIdx.x] = b.second();
     }
     __syncthreads();
-#pragma unroll
-    for (int e = 0; e < 8; ++e) inv[e] = top[0][cv * 8 + e];
   }
   if constexpr (!TR) {
 #pragma unroll
@@ -217,26 +262,51 @@ __device__ __forceinline__ void tile_block(TileShared<TILE, TR>& sh, const XT* _
         float x[8], q[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = v[i].at(e);
-        fp8_quotients<sizeof(XT) == 4>(x, inv[0], all_top, q);
+        const bool close = all.quotients(x, q);
         c.x = fp8_pack4(q[0], q[1], q[2], q[3]);
         c.y = fp8_pack4(q[4], q[5], q[6], q[7]);
         uint8_t* to = Q + (r0 + i) * ldq + c0;
         if (LAST && nc < 8 && r0 + i + 1 == R) store_last(to, c.x, c.y, nc);
         else *reinterpret_cast<uint2*>(to) = c;
+        if (close) fp8_codes_decided(X + (r0 + i) * C + c0, 1, nc, all, to);
       }
     }
   } else {
     auto& turned = sh.turned;
+    auto column = [&](int e) {
+      return Fp8Block<XT>(sh.column[0][cv * 8 + e], sh.column[1][cv * 8 + e]);
+    };
+    // (fp32: all eight at once, in four loads; bf16 has no registers for them)
+    float b0[8], b1[8];
+    if constexpr (!TILE && sizeof(XT) == 4) {
+#pragma unroll
+      for (int e = 0; e < 8; e += 4) {
+        *reinterpret_cast<float4*>(b0 + e) =
+            *reinterpret_cast<const float4*>(&sh.column[0][cv * 8 + e]);
+        *reinterpret_cast<float4*>(b1 + e) =
+            *reinterpret_cast<const float4*>(&sh.column[1][cv * 8 + e]);
+      }
+    }
+    uint32_t close = 0;  // columns of this thread with codes to decide
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       uint2 c;
       float x[8], q[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = v[i].at(e);
-      fp8_quotients<sizeof(XT) == 4>(x, inv[e], TILE ? all_top : most_of[cv * 8 + e], q);
+      const Fp8Block<XT> b =
+          TILE ? all : sizeof(XT) == 4 ? Fp8Block<XT>(b0[e], b1[e]) : column(e);
+      if (b.quotients(x, q)) close |= 1u << e;
       c.x = fp8_pack4(q[0], q[1], q[2], q[3]);
       c.y = fp8_pack4(q[4], q[5], q[6], q[7]);
       turned[cv * 8 + e][rr ^ cv] = c;
+    }
+    for (; close; close &= close - 1) {
+      const int e = __ffs(close) - 1;
+      if (c0 + e < C && r0 < R)
+        fp8_codes_decided(X + r0 * C + c0 + e, C, (int)min((int64_t)8, R - r0),
+                          TILE ? all : column(e),
+                          reinterpret_cast<uint8_t*>(&turned[cv * 8 + e][rr ^ cv]));
     }
     __syncthreads();
 #pragma unroll
@@ -258,11 +328,15 @@ __device__ __forceinline__ void tile_block(TileShared<TILE, TR>& sh, const XT* _
     }
   }
 }
+// Blocks of an SM, bf16: four, or three for turned tiles (32749 x 1000: rows
+// turned 21.3 us with three and 19.8 with four, tiles 20.9 and 22.6); fp32: three
+// where the tile is turned (34.2 with two and 31.0), else two (31.4 and 33.5 with
+// three).
 template <typename XT, bool TILE, bool TR>
-__global__ void __launch_bounds__(256, sizeof(XT) == 2 ? 3 : 2)
+__global__ void __launch_bounds__(256, sizeof(XT) == 2 ? (TILE && TR ? 3 : 4) : TR ? 3 : 2)
 fp8_tile_kernel(const XT* __restrict__ X, uint8_t* __restrict__ Q, float* __restrict__ S,
                 int64_t R, int64_t C, int64_t ldq, int64_t rblocks, int64_t cblocks, int vec) {
-  __shared__ TileShared<TILE, TR> sh;
+  __shared__ TileShared<XT, TILE, TR> sh;
   if (blockIdx.x + 1 < gridDim.x)
     tile_block<XT, TILE, TR, false>(sh, X, Q, S, R, C, ldq, rblocks, cblocks, vec);
   else

@@ -124,7 +124,7 @@ __device__ __noinline__ void norm_decide(const float* h, const float* w, float* 
 #pragma unroll
   for (int i = 0; i < N; ++i)
     if (fp8_near<6>(fp8_from_middle<6>(q[i])))
-      q[i] = fp8_side(q[i], 448.0 * fabs((double)h[i] * (double)w[i]) - fp8_middle(q[i]) * most);
+      q[i] = fp8_side(q[i], 448.0 * fabs((double)h[i] * (double)w[i]) - (double)fp8_middle(q[i]) * most);
 }
 template <int N, int LANES>
 __device__ __forceinline__ void norm_quotients(const float (&y)[N], const float (&h)[N],

@@ -63,3 +63,44 @@ def test_norm_writes_nothing_behind_a_row(R, C, dt, form):
     got, s, _ = kdn.kdn_rmsnorm_forward(x, w, out_dtype=E4M3, y=y)
     assert got is y and torch.equal(s, s_want) and torch.equal(y.float(), want.float())
     assert bool((room[outside | gaps] == GUARD).all())
+
+
+def _exact_codes(v, tile):
+    """The codes of the exact quotients 448 v / magnitude, ties to the even one.
+    (448 v is exact in fp64, the magnitude is one of the values, and a tie's
+    quotient has five bits, so it is seen as one; another quotient of bf16 numbers
+    is 2^-13 of itself away from a tie.)"""
+    rows, cols = v.shape
+    p = np.pad(np.abs(v), ((0, -rows % 128 if tile else 0), (0, -cols % 128)))
+    top = p.reshape(-1, 128 if tile else 1, p.shape[1] // 128, 128).max((1, 3))
+    top = fp8_ref.spread(np.maximum(top, fp8_ref.FLOOR), rows, cols, tile)
+    return fp8_ref.e4m3(448.0 * v / top)
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+def test_codes_of_bf16_round_ties_to_even_in_rows(transpose):
+    """Every significand of a value against every one of its block's largest, over
+    the exponents that give codes: blocks of one largest and 127 others."""
+    m = torch.arange(128, 256, dtype=torch.float64)
+    v = (m[:, None] * 2.0 ** -torch.arange(8, 29)).flatten()          # below every m, to codes of 0
+    v = torch.cat([v, v.new_zeros(-len(v) % 127)]).reshape(-1, 127)
+    x = torch.cat([m[:, None, None].expand(-1, len(v), 1), v.expand(128, -1, -1)], 2).reshape(128, -1)
+    x = (x * torch.where(torch.arange(x.shape[1]) % 3 == 1, -1.0, 1.0)).bfloat16().cuda()
+    for part in (x, x[:, :x.shape[1] - 3].contiguous()):                # whole pieces, and not
+        q, _ = kdn.kdn_fp8_quantize(part.t().contiguous() if transpose else part, transpose=transpose)
+        np.testing.assert_array_equal(f64(q.float()), _exact_codes(f64(part), False))
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+def test_codes_of_bf16_round_ties_to_even_in_tiles(transpose):
+    """A tile for every significand of the largest value."""
+    g = torch.Generator().manual_seed(3)
+    v = torch.randint(128, 256, (1024, 2048), generator=g) * 2.0 ** -torch.randint(8, 24, (1024, 2048),
+                                                                                  generator=g)
+    v = v.double()
+    for i, m in enumerate(range(128, 256)):
+        v[i // 16 * 128 + i % 100, i % 16 * 128 + i % 77] = -m
+    x = v.bfloat16().cuda()
+    q, _ = kdn.kdn_fp8_quantize(x, tile=True, transpose=transpose)
+    want = _exact_codes(f64(x).T if transpose else f64(x), True)
+    np.testing.assert_array_equal(f64(q.float()), want)
