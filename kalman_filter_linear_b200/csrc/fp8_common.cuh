@@ -40,7 +40,11 @@ __device__ __forceinline__ uint32_t fp8_pack4(float q0, float q1, float q2, floa
 // so near the middle between two codes it may be the other one.  The middle of
 // two normal codes has the bits 1000... below the third of the fraction;
 // fp8_near tells whether a quotient is within ULPS units in the last place of
-// it, and such a quotient is decided again in fp64.
+// it, and such a quotient is decided again in fp64.  Below 2^-6, the smallest
+// normal code, codes are 2^-9 apart whatever the exponent: 2^-6 added (lifted),
+// their middles have the same bits, and the few units of a smaller quotient are
+// fewer of the sum's.
+constexpr float kE4m3Normal = 0.015625f;  // 2^-6
 template <uint32_t ULPS>
 __device__ __forceinline__ uint32_t fp8_from_middle(float q) {
   return __float_as_uint(q) * 4096u + ((ULPS - 0x80000u) << 12);
@@ -49,16 +53,34 @@ template <uint32_t ULPS>
 __device__ __forceinline__ bool fp8_near(uint32_t from_middle) {
   return from_middle <= 2u * ULPS << 12;
 }
+template <uint32_t ULPS>
+__device__ __forceinline__ bool fp8_near_lifted(float q) {
+  const float m = fabsf(q);
+  return fp8_near<ULPS>(fp8_from_middle<ULPS>(m < kE4m3Normal ? m + kE4m3Normal : m));
+}
+// Whether any of the quotients is near a middle (or seems to be: a normal one that
+// is lifted all the same, where another is small, may ask without need).  Small
+// ones are looked for first: a lift for each of them cost 3 % of fp32 rows.
 template <uint32_t ULPS, int N>
 __device__ __forceinline__ bool fp8_any_near(const float (&q)[N]) {
   uint32_t near = ~0u;
+  float least = kE4m3Normal;
 #pragma unroll
   for (int i = 0; i < N; ++i) near = min(near, fp8_from_middle<ULPS>(q[i]));
+#pragma unroll
+  for (int i = 0; i < N; ++i) least = fminf(least, fabsf(q[i]));
+  if (least < kE4m3Normal) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      near = min(near, fp8_from_middle<ULPS>(fabsf(q[i]) + kE4m3Normal));
+  }
   return fp8_near<ULPS>(near);
 }
 // The middle of the two codes that q is between, as a float (it is one).
 __device__ __forceinline__ float fp8_middle(float q) {
-  return fabsf(__uint_as_float((__float_as_uint(q) & 0xfff00000u) | 0x80000u));
+  const float m = fabsf(q);
+  return m < kE4m3Normal ? (floorf(m * 512.f) + 0.5f) / 512.f
+                         : __uint_as_float((__float_as_uint(m) & 0xfff00000u) | 0x80000u);
 }
 // The float nearest to q on the side of its middle that the exact quotient is
 // on; over: the sign of the exact magnitude less the middle's.

@@ -31,7 +31,7 @@ __device__ __noinline__ void fp8_codes_decided(const float* x, int64_t step, int
     uint32_t which = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i0 + i < n && fp8_near<2>(fp8_from_middle<2>(x[(i0 + i) * step] * b.inv))) which |= 1u << i;
+      if (i0 + i < n && fp8_near_lifted<2>(x[(i0 + i) * step] * b.inv)) which |= 1u << i;
     for (; which; which &= which - 1) {
       const int i = i0 + __ffs(which) - 1;
       const float v = x[i * step];

@@ -123,20 +123,16 @@ __device__ __noinline__ void norm_decide(const float* h, const float* w, float* 
   for (int o = LANES / 2; o > 0; o >>= 1) most = fmax(most, __shfl_xor_sync(0xffffffffu, most, o));
 #pragma unroll
   for (int i = 0; i < N; ++i)
-    if (fp8_near<6>(fp8_from_middle<6>(q[i])))
+    if (fp8_near_lifted<6>(q[i]))
       q[i] = fp8_side(q[i], 448.0 * fabs((double)h[i] * (double)w[i]) - (double)fp8_middle(q[i]) * most);
 }
 template <int N, int LANES>
 __device__ __forceinline__ void norm_quotients(const float (&y)[N], const float (&h)[N],
                                                const float (&w)[N], float top, float (&q)[N]) {
   const float inv = fp8_inverse(top);
-  uint32_t near = ~0u;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    q[i] = y[i] * inv;
-    near = min(near, fp8_from_middle<6>(q[i]));
-  }
-  if (!__any_sync(0xffffffffu, fp8_near<6>(near))) return;
+  for (int i = 0; i < N; ++i) q[i] = y[i] * inv;
+  if (!__any_sync(0xffffffffu, fp8_any_near<6>(q))) return;
   float a[N], b[N], c[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {

@@ -104,3 +104,49 @@ def test_codes_of_bf16_round_ties_to_even_in_tiles(transpose):
     q, _ = kdn.kdn_fp8_quantize(x, tile=True, transpose=transpose)
     want = _exact_codes(f64(x).T if transpose else f64(x), True)
     np.testing.assert_array_equal(f64(q.float()), want)
+
+
+def _next_to_middles(rows, blocks, seed):
+    """fp32 blocks of 128: their largest value, then for each middle of two codes
+    below 2^-6 and some above it the five numbers whose quotients are nearest."""
+    rng = np.random.default_rng(seed)
+    top = rng.uniform(1, 2, (rows, blocks, 1)).astype(np.float32)
+    mid = np.concatenate([(2 * np.arange(8) + 1) * 2.0 ** -10,
+                          (2 * rng.integers(8, 16, 17) + 1) * 2.0 ** rng.integers(-10, 3, 17)])
+    v = (mid * top.astype(np.float64) / 448.0).astype(np.float32)
+    v = (v.view(np.int32)[..., None] + np.arange(-2, 3, dtype=np.int32)).view(np.float32)
+    v = np.concatenate([top, v.reshape(rows, blocks, 125), np.zeros((rows, blocks, 2))], 2)
+    return (v * rng.choice([-1.0, 1.0], v.shape)).astype(np.float32)
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("cols", [1024, 1016, 1003])
+def test_codes_of_fp32_next_to_middles_in_rows(cols, transpose):
+    x = torch.from_numpy(_next_to_middles(512, 8, cols).reshape(512, 1024)[:, :cols].copy()).cuda()
+    q, _ = kdn.kdn_fp8_quantize(x.t().contiguous() if transpose else x, transpose=transpose)
+    np.testing.assert_array_equal(f64(q.float()), _exact_codes(f64(x), False))
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+def test_codes_of_fp32_next_to_middles_in_tiles(transpose):
+    v = _next_to_middles(1, 64, 5).reshape(8, 8, 1, 128)
+    x = np.repeat(v, 128, 2)
+    x[:, :, 1:, 0] = 0
+    x = torch.from_numpy(x.transpose(0, 2, 1, 3).reshape(1024, 1024).copy()).cuda()
+    q, _ = kdn.kdn_fp8_quantize(x.t().contiguous() if transpose else x, tile=True, transpose=transpose)
+    np.testing.assert_array_equal(f64(q.float()), _exact_codes(f64(x), True))
+
+
+@pytest.mark.parametrize("cols", [128, 1024, 1003, 4096])
+@pytest.mark.parametrize("weighted", [False, True])
+def test_codes_of_the_norm_next_to_middles(cols, weighted):
+    """The factor 1 / rms is the same in a whole row, so a code is that of 448 h w
+    over the block's largest |h w|."""
+    rng = np.random.default_rng(cols)
+    v = _next_to_middles(256, 32, cols).reshape(256, 4096)[:, :cols]
+    w = rng.uniform(0.5, 2, cols).astype(np.float32) if weighted else np.ones(cols, np.float32)
+    w[::128] = 2.0                                       # (the largest stays so)
+    h = (v.astype(np.float64) / w).astype(np.float32)
+    y, _, _ = kdn.kdn_rmsnorm_forward(torch.from_numpy(h).cuda(), torch.from_numpy(w).cuda(),
+                                      out_dtype=E4M3)
+    np.testing.assert_array_equal(f64(y.float()), _exact_codes(h.astype(np.float64) * w, False))
