@@ -879,10 +879,8 @@ kdn_status wide_go(const void* x, int64_t ldx, const void* w, int64_t ldw, int K
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fp8_matmul_wide<BN, TILE, OT>, mx, mw, mo, p, tn, (int)tiles) ==
-                 cudaSuccess
-             ? KDN_OK
-             : KDN_ERR_CUDA;
+  return enqueued(
+      cudaLaunchKernelEx(&cfg, fp8_matmul_wide<BN, TILE, OT>, mx, mw, mo, p, tn, (int)tiles));
 }
 
 template <int BT, bool TILE, typename OT>
@@ -916,10 +914,7 @@ kdn_status few_go(const void* x, int64_t ldx, const void* w, int64_t ldw, int K,
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fp8_matmul_few<BT, TILE, OT>, mx, mw, p, tn, split) ==
-                 cudaSuccess
-             ? KDN_OK
-             : KDN_ERR_CUDA;
+  return enqueued(cudaLaunchKernelEx(&cfg, fp8_matmul_few<BT, TILE, OT>, mx, mw, p, tn, split));
 }
 
 template <bool TILE, typename OT>

@@ -350,25 +350,15 @@ kdn_status quantize_types(const void* x, void* q, float* scale, int64_t R, int64
   uint8_t* Q = static_cast<uint8_t*>(q);
   const int64_t rb = (R + 127) / 128, cb = (C + 127) / 128;
   const int vec = C % 8 == 0;
-  if (!tile && !tr && C % 16 == 0)
-    fp8_rows_kernel<XT, false><<<(unsigned)((R * cb * 8 + 127) / 128), 128, 0, s>>>(
-        X, Q, scale, R, (int)C, ldq, (int)cb);
-  else if (!tile && !tr && vec)
-    fp8_rows_kernel<XT, true><<<(unsigned)((R * cb * 8 + 127) / 128), 128, 0, s>>>(
-        X, Q, scale, R, (int)C, ldq, (int)cb);
-  else if (!tile && !tr)
-    fp8_rows_any_kernel<XT><<<(unsigned)((R * cb * 16 + 255) / 256), 256, 0, s>>>(
-        X, Q, scale, R, (int)C, ldq, (int)cb);
-  else if (tile && !tr)
-    fp8_tile_kernel<XT, true, false><<<(unsigned)(rb * cb), 256, 0, s>>>(X, Q, scale, R, C, ldq,
-                                                                         rb, cb, vec);
-  else if (tile)
-    fp8_tile_kernel<XT, true, true><<<(unsigned)(rb * cb), 256, 0, s>>>(X, Q, scale, R, C, ldq, rb,
-                                                                        cb, vec);
-  else
-    fp8_tile_kernel<XT, false, true><<<(unsigned)(rb * cb), 256, 0, s>>>(X, Q, scale, R, C, ldq,
-                                                                         rb, cb, vec);
-  return cudaGetLastError() == cudaSuccess ? KDN_OK : KDN_ERR_CUDA;
+  if (!tile && !tr && vec)
+    return launch(C % 16 == 0 ? fp8_rows_kernel<XT, false> : fp8_rows_kernel<XT, true>,
+                  (R * cb * 8 + 127) / 128, 128, 0, s, X, Q, scale, R, (int)C, ldq, (int)cb);
+  if (!tile && !tr)
+    return launch(fp8_rows_any_kernel<XT>, (R * cb * 16 + 255) / 256, 256, 0, s, X, Q, scale, R,
+                  (int)C, ldq, (int)cb);
+  return launch(!tile ? fp8_tile_kernel<XT, false, true>
+                      : tr ? fp8_tile_kernel<XT, true, true> : fp8_tile_kernel<XT, true, false>,
+                rb * cb, 256, 0, s, X, Q, scale, R, C, ldq, rb, cb, vec);
 }
 
 }  // namespace

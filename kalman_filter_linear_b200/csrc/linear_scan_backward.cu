@@ -170,15 +170,16 @@ kdn_status backward_go(const LsCall& k) {
   const LsPlan p = ls_plan(k.B, k.T, k.D, kLsBwdSteps * kLsWarps);
   const LsWs ws = ls_ws(k.workspace, p);
   // error word, tile counter and flags (one step range: the kernel itself)
-  if (p.chunks > 1 && cudaMemsetAsync(k.workspace, 0, p.map, k.stream) != cudaSuccess)
-    return KDN_ERR_CUDA;
-  linear_scan_backward_kernel<GT, XT, HAS_B, PACKED, EVEN>
-      <<<(unsigned)(p.chunks * p.cols), kLsThreads, 0, k.stream>>>(
-          static_cast<const GT*>(k.a), static_cast<const GT*>(k.b), static_cast<const XT*>(k.x),
-          static_cast<const XT*>(k.y), static_cast<const XT*>(k.dy), k.h0, k.end_in,
-          static_cast<GT*>(k.da), static_cast<GT*>(k.db), static_cast<XT*>(k.dx), k.end_out, k.cu,
-          k.N, k.T, k.D, (int)(p.cols / k.B), p.chunks, p.cols, ws);
-  return cudaGetLastError() == cudaSuccess ? KDN_OK : KDN_ERR_CUDA;
+  if (p.chunks > 1) {
+    const kdn_status st = enqueued(cudaMemsetAsync(k.workspace, 0, p.map, k.stream));
+    if (st != KDN_OK) return st;
+  }
+  return launch(linear_scan_backward_kernel<GT, XT, HAS_B, PACKED, EVEN>, p.chunks * p.cols,
+                kLsThreads, 0, k.stream, static_cast<const GT*>(k.a), static_cast<const GT*>(k.b),
+                static_cast<const XT*>(k.x), static_cast<const XT*>(k.y),
+                static_cast<const XT*>(k.dy), k.h0, k.end_in, static_cast<GT*>(k.da),
+                static_cast<GT*>(k.db), static_cast<XT*>(k.dx), k.end_out, k.cu, k.N, k.T, k.D,
+                (int)(p.cols / k.B), p.chunks, p.cols, ws);
 }
 
 template <typename GT, typename XT>

@@ -180,10 +180,9 @@ template <typename GT, typename XT, bool HAS_B>
 kdn_status step_launch(const void* a, const void* b, const void* x, float* h, void* y, int64_t n,
                        cudaStream_t s) {
   const int64_t blocks = (n + 511) / 512;
-  linear_scan_step_kernel<GT, XT, HAS_B><<<(unsigned)blocks, 128, 0, s>>>(
-      static_cast<const GT*>(a), static_cast<const GT*>(b), static_cast<const XT*>(x), h,
-      static_cast<XT*>(y), n);
-  return cudaGetLastError() == cudaSuccess ? KDN_OK : KDN_ERR_CUDA;
+  return launch(linear_scan_step_kernel<GT, XT, HAS_B>, blocks, 128, 0, s,
+                static_cast<const GT*>(a), static_cast<const GT*>(b), static_cast<const XT*>(x), h,
+                static_cast<XT*>(y), n);
 }
 
 template <typename GT, typename XT, bool HAS_B, bool PACKED, bool EVEN>
@@ -191,14 +190,14 @@ kdn_status forward_go(const LsCall& k) {
   const LsPlan p = ls_plan(k.B, k.T, k.D, kLsFwdSteps * kLsWarps);
   const LsWs ws = ls_ws(k.workspace, p);
   // error word, tile counter and flags (one step range: the kernel itself)
-  if (p.chunks > 1 && cudaMemsetAsync(k.workspace, 0, p.map, k.stream) != cudaSuccess)
-    return KDN_ERR_CUDA;
-  linear_scan_forward_kernel<GT, XT, HAS_B, PACKED, EVEN>
-      <<<(unsigned)(p.chunks * p.cols), kLsThreads, 0, k.stream>>>(
-          static_cast<const GT*>(k.a), static_cast<const GT*>(k.b), static_cast<const XT*>(k.x),
-          k.h0, static_cast<XT*>(k.y_out), k.end_out, k.cu, k.N, k.T, k.D, (int)(p.cols / k.B),
-          p.chunks, p.cols, ws);
-  return cudaGetLastError() == cudaSuccess ? KDN_OK : KDN_ERR_CUDA;
+  if (p.chunks > 1) {
+    const kdn_status st = enqueued(cudaMemsetAsync(k.workspace, 0, p.map, k.stream));
+    if (st != KDN_OK) return st;
+  }
+  return launch(linear_scan_forward_kernel<GT, XT, HAS_B, PACKED, EVEN>, p.chunks * p.cols,
+                kLsThreads, 0, k.stream, static_cast<const GT*>(k.a), static_cast<const GT*>(k.b),
+                static_cast<const XT*>(k.x), k.h0, static_cast<XT*>(k.y_out), k.end_out, k.cu, k.N,
+                k.T, k.D, (int)(p.cols / k.B), p.chunks, p.cols, ws);
 }
 
 template <typename GT, typename XT>

@@ -819,9 +819,7 @@ kdn_status ls_stream_go(const void* a, const void* x, const void* y, const void*
   }
   cfg.gridDim = dim3((unsigned)(clusters * C));
   at[0].val.clusterDim.x = (unsigned)C;
-  return cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], m[3], m[4], p) == cudaSuccess
-             ? KDN_OK
-             : KDN_ERR_CUDA;
+  return enqueued(cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], m[3], m[4], p));
 }
 
 // Whether a call streams.  With packed sequences the second pass reads the

@@ -436,11 +436,9 @@ kdn_status fwd_go(const FwdArgs& a, cudaStream_t s) {
   using S = Shape<G, NV, VEC>;
   const int64_t want = (a.rows + S::ROWS - 1) / S::ROWS, most = resident(S::BLOCKS);
   if (most == 0) return KDN_ERR_CUDA;
-  rmsnorm_forward_kernel<XT, RT, RES, OUT, G, NV, VEC>
-      <<<(unsigned)(want < most ? want : most), S::THREADS, 0, s>>>(
-          static_cast<const XT*>(a.x), static_cast<const RT*>(a.res), a.w, static_cast<RT*>(a.h),
-          a.y, a.scale, a.rows, a.D, a.ldy, a.eps);
-  return cudaGetLastError() == cudaSuccess ? KDN_OK : KDN_ERR_CUDA;
+  return launch(rmsnorm_forward_kernel<XT, RT, RES, OUT, G, NV, VEC>, want < most ? want : most,
+                S::THREADS, 0, s, static_cast<const XT*>(a.x), static_cast<const RT*>(a.res), a.w,
+                static_cast<RT*>(a.h), a.y, a.scale, a.rows, a.D, a.ldy, a.eps);
 }
 template <typename XT, typename RT, bool RES, Out OUT, bool VEC>
 kdn_status fwd_size(const FwdArgs& a, cudaStream_t s) {
@@ -484,14 +482,14 @@ kdn_status bwd_go(const BwdArgs& a, cudaStream_t s) {
   const int blocks = (int)(want < most ? want : most);
   const size_t smem = S::ROWS > 1 ? (size_t)S::ROWS * a.D * 4 : 0;
   if (blocks > 0) {
-    rmsnorm_backward_kernel<HT, YT, XT, G, NV, VEC><<<blocks, S::THREADS, smem, s>>>(
+    const kdn_status st = launch(
+        rmsnorm_backward_kernel<HT, YT, XT, G, NV, VEC>, blocks, S::THREADS, smem, s,
         static_cast<const HT*>(a.h), a.w, static_cast<const YT*>(a.dy),
         static_cast<const HT*>(a.dh), static_cast<XT*>(a.dx), static_cast<HT*>(a.dres), a.part,
         a.rows, a.D, a.eps);
-    if (cudaGetLastError() != cudaSuccess) return KDN_ERR_CUDA;
+    if (st != KDN_OK) return st;
   }
-  rmsnorm_dweight_kernel<<<(a.D + 31) / 32, 1024, 0, s>>>(a.part, a.dw, blocks, a.D);
-  return cudaGetLastError() == cudaSuccess ? KDN_OK : KDN_ERR_CUDA;
+  return launch(rmsnorm_dweight_kernel, (a.D + 31) / 32, 1024, 0, s, a.part, a.dw, blocks, a.D);
 }
 template <typename HT, typename YT, typename XT, bool VEC>
 kdn_status bwd_size(const BwdArgs& a, cudaStream_t s) {
