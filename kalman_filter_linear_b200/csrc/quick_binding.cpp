@@ -3,8 +3,9 @@
 // C entry point, in one C++ function each (a small call is bound by its host
 // side: scan step 10.4 us through ctypes, norm of 256 rows 13.8).  A function
 // returns None for anything out of the ordinary, an argument that a check
-// refuses or a status that is not KDN_OK, and has then enqueued nothing; kdn.py
-// goes on in Python, which finds the words for it.
+// refuses, and has then enqueued nothing; kdn.py goes on in Python, which finds
+// the words for it.  An error of the CUDA runtime is raised here: something may
+// have been enqueued before it, and is not enqueued again.
 #include <Python.h>
 
 #include <ATen/Functions.h>
@@ -21,6 +22,10 @@ using at::ScalarType;
 using at::Tensor;
 
 struct Unusual {};
+struct Failed {
+  kdn_status status;
+  const char* where;
+};
 
 constexpr ScalarType F32 = ScalarType::Float, BF16 = ScalarType::BFloat16,
                      E4M3 = ScalarType::Float8_e4m3fn;
@@ -31,11 +36,23 @@ void usual(bool ok) {
 // An entry point's call, without the interpreter's lock (a launch waits when
 // the stream's queue is full).
 template <typename F, typename... A>
-void call(F f, A... args) {
+void call(const char* name, F f, A... args) {
   PyThreadState* s = PyEval_SaveThread();
   const kdn_status st = f(args...);
   PyEval_RestoreThread(s);
-  usual(st == KDN_OK);
+  usual(st != KDN_ERR_INVALID_ARG && st != KDN_ERR_UNSUPPORTED && st != KDN_ERR_WORKSPACE);
+  if (st != KDN_OK) throw Failed{st, name};
+}
+#define KDN_CALL(f, ...) call(#f, f, __VA_ARGS__)
+// kdn.KdnError
+void raise(const Failed& e) {
+  PyObject* module = PyImport_ImportModule("kalman_filter_linear_b200.kdn");
+  PyObject* type = module ? PyObject_GetAttrString(module, "KdnError") : nullptr;
+  PyObject* error = type ? PyObject_CallFunction(type, "is", (int)e.status, e.where) : nullptr;
+  if (error) PyErr_SetObject(type, error);
+  Py_XDECREF(error);
+  Py_XDECREF(type);
+  Py_XDECREF(module);
 }
 const Tensor* opt(PyObject* o) {
   if (o == Py_None) return nullptr;
@@ -128,7 +145,7 @@ PyObject* scan_step(PyObject* const* v) {
   void *pa = p.arg(&a, a.scalar_type(), shape), *pb = p.arg(b, a.scalar_type(), shape);
   void *px = p.arg(&x, x.scalar_type(), shape), *ph = p.arg(&h, F32, shape);
   Tensor y = p.out(v[4], x.scalar_type(), shape);
-  call(kdn_linear_scan_step, pa, pb, gate, px, in, static_cast<float*>(ph), y.data_ptr(),
+  KDN_CALL(kdn_linear_scan_step, pa, pb, gate, px, in, static_cast<float*>(ph), y.data_ptr(),
                              (int)shape[0], (int)shape[1], p.stream());
   return wrap(y);
 }
@@ -145,7 +162,7 @@ PyObject* scan_forward(PyObject* const* v) {
   void* pc = p.arg(cu, ScalarType::Int, {d.B + 1});
   Tensor y = p.out(v[5], xt, shape), h = p.out(v[6], F32, {d.B, d.D});
   Tensor ws = scan_workspace(p, d.bytes);
-  call(kdn_linear_scan_forward, a.data_ptr(), pb, gate, px, in, static_cast<float*>(p0),
+  KDN_CALL(kdn_linear_scan_forward, a.data_ptr(), pb, gate, px, in, static_cast<float*>(p0),
                                 static_cast<int32_t*>(pc), y.data_ptr(), h.data_ptr<float>(),
                                 (int)d.B, (int)d.T, (int)d.D, ws.data_ptr(), (size_t)ws.numel(),
                                 p.stream());
@@ -168,7 +185,7 @@ PyObject* scan_backward(PyObject* const* v) {
   Tensor da = p.out(v[8], gt, shape), dx = p.out(v[9], yt, shape), db;
   if (b) db = p.out(v[10], gt, shape);
   Tensor dh0 = p.out(v[11], F32, {d.B, d.D}), ws = scan_workspace(p, d.bytes);
-  call(kdn_linear_scan_backward, a.data_ptr(), pb, gate, px, py, pdy, in, static_cast<float*>(p0),
+  KDN_CALL(kdn_linear_scan_backward, a.data_ptr(), pb, gate, px, py, pdy, in, static_cast<float*>(p0),
             static_cast<float*>(pT), static_cast<int32_t*>(pc), da.data_ptr(),
             b ? db.data_ptr() : nullptr, dx.data_ptr(), dh0.data_ptr<float>(), (int)d.B, (int)d.T,
             (int)d.D, ws.data_ptr(), (size_t)ws.numel(), p.stream());
@@ -224,7 +241,7 @@ PyObject* norm_forward(PyObject* const* v) {
   } else {
     y = p.out(v[5], out, shape);
   }
-  call(kdn_rmsnorm_forward, px, xt, pr, rt, static_cast<float*>(pw), res ? h.data_ptr() : nullptr,
+  KDN_CALL(kdn_rmsnorm_forward, px, xt, pr, rt, static_cast<float*>(pw), res ? h.data_ptr() : nullptr,
                             y.data_ptr(), (kdn_dtype)whole(v[4]), ld,
                             out == E4M3 ? scale.data_ptr<float>() : nullptr, rows, (int)D,
                             real(v[3]), p.stream());
@@ -257,7 +274,7 @@ PyObject* norm_backward(PyObject* const* v) {
   if (want) dres = p.out(v[8], ht, shape);
   const size_t bytes = kdn_rmsnorm_backward_workspace_size(rows, (int)D);
   Tensor ws = p.empty({(int64_t)bytes}, ScalarType::Byte);
-  call(kdn_rmsnorm_backward, ph, hc, static_cast<float*>(pw), pdy, yc, pdh, dx.data_ptr(),
+  KDN_CALL(kdn_rmsnorm_backward, ph, hc, static_cast<float*>(pw), pdy, yc, pdh, dx.data_ptr(),
                              xt == F32 ? KDN_F32 : KDN_BF16, want ? dres.data_ptr() : nullptr,
                              dw.data_ptr<float>(), rows, (int)D, real(v[4]), ws.data_ptr(), bytes,
                              p.stream());
@@ -285,7 +302,7 @@ PyObject* quantize(PyObject* const* v) {
   int64_t ld = 0;
   void* pq = p.fp8(q, R, C, &ld);
   Tensor s = p.out(v[4], F32, {tile ? (R + 127) / 128 : R, (C + 127) / 128});
-  call(kdn_fp8_quantize, px, xt, rows, cols, tile, tr, pq, ld, s.data_ptr<float>(), p.stream());
+  KDN_CALL(kdn_fp8_quantize, px, xt, rows, cols, tile, tr, pq, ld, s.data_ptr<float>(), p.stream());
   return Py_BuildValue("(NN)", wrap(q), wrap(s));
 }
 
@@ -304,7 +321,7 @@ PyObject* matmul(PyObject* const* v) {
   usual(ot != E4M3);
   Tensor out = p.out(v[5], ot, {M, N});
   void* st = p.arg(opt(v[6]), ScalarType::Int, {1});
-  call(kdn_fp8_matmul, px, ldx, static_cast<float*>(psx), pw, ldw, static_cast<float*>(psw), tile,
+  KDN_CALL(kdn_fp8_matmul, px, ldx, static_cast<float*>(psx), pw, ldw, static_cast<float*>(psw), tile,
                        out.data_ptr(), ot == F32 ? KDN_F32 : KDN_BF16, (int)M, (int)N, (int)K,
                        static_cast<uint32_t*>(st), p.stream());
   return wrap(out);
@@ -315,6 +332,9 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n == N) {
     try {
       return F(args);
+    } catch (const Failed& e) {
+      raise(e);
+      return nullptr;
     } catch (...) {
     }
     PyErr_Clear();

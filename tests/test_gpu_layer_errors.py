@@ -80,3 +80,34 @@ def test_a_step_in_place_is_one_step(form, runtime):
     kdn.kdn_rmsnorm_backward(x, x[0], dy, dh=dh, dresidual=dh)
     runtime.cudaGetLastError()
     assert torch.equal(dh, want)
+
+
+def test_a_call_that_fails_is_not_made_again(monkeypatch, runtime):
+    """On a stream whose capture has been invalidated (a synchronisation is not
+    allowed in one) a launch is an error; the Python form is not tried then."""
+    a, x = torch.full((2, 8), 0.5, device='cuda'), torch.ones(2, 8, device='cuda')
+    h, y = torch.zeros(2, 8, device='cuda'), torch.empty(2, 8, device='cuda')
+    kdn.kdn_linear_scan_step(a, x, h, y=y)
+    side = torch.cuda.Stream()
+    handle, graph = ctypes.c_void_p(side.cuda_stream), ctypes.c_void_p()
+    torch.cuda.synchronize()
+
+    def again(*args):
+        raise AssertionError('the call was made a second time')
+
+    monkeypatch.setattr(kdn, '_call', again)
+    assert kdn._load_quick() is not kdn._NoQuick
+    assert runtime.cudaStreamBeginCapture(handle, 2) == 0       # 2: relaxed
+    try:
+        assert runtime.cudaStreamSynchronize(handle) != 0
+        with torch.cuda.stream(side), pytest.raises(kdn.KdnError) as e:
+            kdn.kdn_linear_scan_step(a, x, h, y=y)
+    finally:
+        runtime.cudaStreamEndCapture(handle, ctypes.byref(graph))
+    assert e.value.status == kdn.KDN_ERR_CUDA
+    assert 'kdn_linear_scan_step' in str(e.value)
+    runtime.cudaGetLastError()
+    torch.cuda.synchronize()
+    assert bool((h == 1).all())
+    kdn._quick.scan_step(a, x, h, None, y)
+    assert bool((h == 1.5).all())
