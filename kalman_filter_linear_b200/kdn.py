@@ -772,6 +772,8 @@ def _fp8_arg(q, name, rows, cols, dev):
         raise ValueError(f'{name} must have shape {(rows, cols)}, got {tuple(q.shape)}')
     if q.device != dev:
         raise ValueError(f'{name} must be on {dev}, got {q.device}')
+    if rows == 0 or cols == 0:  # (nothing is read or written)
+        return None, 0
     ld = q.stride(0) if rows > 1 else (cols + 15) // 16 * 16
     if (cols > 1 and q.stride(1) != 1) or ld % 16 or ld < cols:
         raise ValueError(f'the rows of {name} must be contiguous and a multiple of 16 bytes apart '
@@ -909,7 +911,7 @@ def kdn_fp8_matmul(x, x_scale, w, w_scale, out_dtype=torch.bfloat16, out=None, s
     16-byte boundaries, as kdn_fp8_quantize lays them out), x_scale
     [M, ceil(K / 128)], w_scale [ceil(N / 128), ceil(K / 128)] (128 x 128
     tiles) or [N, ceil(K / 128)], fp32.  Returns [M, N] in out_dtype (bfloat16
-    or float32).  status: one zeroed int32 word that a timed-out wait sets."""
+    or float32): zeros for K = 0.  status: one zeroed int32 word that a timed-out wait sets."""
     r = (_quick or _load_quick()).matmul(x, x_scale, w, w_scale, _CODE.get(out_dtype, -1), out, status)
     if r is not None:
         return r
@@ -931,7 +933,9 @@ def kdn_fp8_matmul(x, x_scale, w, w_scale, out_dtype=torch.bfloat16, out=None, s
     out = x.new_empty((M, N), dtype=out_dtype) if out is None else out
     po = _arg(out, 'out', out_dtype, (M, N), dev)
     pst = _arg(status, 'status', torch.int32, (1,), dev)
-    if M:
+    if K == 0:  # a sum over nothing
+        out.zero_()
+    elif M and N:
         st = _call(lib().kdn_fp8_matmul, dev, px, ldx, psx, pw, ldw, psw, int(tile), po,
                    _CODE[out_dtype], M, N, K, pst)
         _check(st, 'kdn_fp8_matmul')

@@ -150,3 +150,37 @@ def test_codes_of_the_norm_next_to_middles(cols, weighted):
     y, _, _ = kdn.kdn_rmsnorm_forward(torch.from_numpy(h).cuda(), torch.from_numpy(w).cuda(),
                                       out_dtype=E4M3)
     np.testing.assert_array_equal(f64(y.float()), _exact_codes(h.astype(np.float64) * w, False))
+
+
+@pytest.mark.parametrize("tile", [False, True])
+def test_empty_matrices(tile, form):
+    """No rows or no columns, either way round; an empty batch's weight gradient
+    is zeros."""
+    blocks = lambda n: -(-n // 128)
+    for shape in ((0, 300), (300, 0), (0, 0), (1, 0), (0, 1)):
+        x = torch.empty(shape, device='cuda')
+        for tr in (False, True):
+            R, C = shape[::-1] if tr else shape
+            q, s = kdn.kdn_fp8_quantize(x, tile=tile, transpose=tr)
+            assert q.shape == (R, C) and q.dtype == E4M3
+            assert s.shape == (blocks(R) if tile else R, blocks(C))
+            q2, _ = kdn.kdn_fp8_quantize(x, tile=tile, transpose=tr, q=q)
+            assert q2 is q
+
+
+def test_products_over_nothing(form):
+    dy, x = torch.empty(0, 300, device='cuda'), torch.empty(0, 40, device='cuda')
+    a, b = (kdn.kdn_fp8_quantize(t, transpose=True) for t in (dy, x))
+    for out in (F32, BF16):
+        room = torch.full((300, 40), 7.0, dtype=out, device='cuda')
+        got = kdn.kdn_fp8_matmul(*a, *b, out_dtype=out, out=room)
+        assert got is room and bool((got == 0).all())
+        assert bool((kdn.kdn_fp8_matmul(*a, *b, out_dtype=out) == 0).all())
+    w = kdn.kdn_fp8_quantize(torch.randn(300, 40, device='cuda'), tile=True)
+    rows = kdn.kdn_fp8_quantize(torch.randn(5, 40, device='cuda'))
+    assert kdn.kdn_fp8_matmul(rows[0][:0], rows[1][:0], *w).shape == (0, 300)
+    assert kdn.kdn_fp8_matmul(*rows, w[0][:0], w[1][:0]).shape == (5, 0)
+    one = (torch.empty(1, 0, device='cuda').to(E4M3), torch.empty(1, 0, device='cuda'))
+    assert bool((kdn.kdn_fp8_matmul(*one, *one) == 0).all())
+    with pytest.raises(ValueError):
+        kdn.kdn_fp8_matmul(*a, b[0], b[1][:3])
