@@ -414,6 +414,9 @@ fp8_matmul_wide(const __grid_constant__ CUtensorMap mx, const __grid_constant__ 
       else tmem_ld_rows16(from + ((uint32_t)(16 * (c & 1)) << 16), r[c & 1]);
     };
     uint32_t g = 0, buf = 0, phase = 0;
+    // Outputs leave by two places in turn, over tiles too: an odd number of pieces
+    // (128 columns in bf16: one a warp) begins a tile where the last one ended.
+    uint32_t pieces = 0;
     bool bad = false;
     for (int tile = pair; tile < tiles && !bad; tile += pairs) {
       const int mw0 = tile / tiles_n * 256 + (int)rank * 128 + 32 * q;
@@ -511,11 +514,11 @@ fp8_matmul_wide(const __grid_constant__ CUtensorMap mx, const __grid_constant__ 
         constexpr int ES = (int)sizeof(OT), PC = 128 / ES;  // columns of a piece
         constexpr int PER = TILE ? 8 / ES : 1;              // pairs that one store takes
 #pragma unroll
-        for (int piece = 0; piece < CW / PC; ++piece) {
+        for (int piece = 0; piece < CW / PC; ++piece, ++pieces) {
           // (the copy before the last one has left its place)
           if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
           __syncwarp();
-          uint8_t* place = stage_out + (piece & 1) * 4096;
+          uint8_t* place = stage_out + (CW / PC % 2 ? pieces & 1u : piece & 1) * 4096;
 #pragma unroll
           for (int c = 0; c < CHUNKS; ++c)
 #pragma unroll

@@ -184,3 +184,27 @@ def test_products_over_nothing(form):
     assert bool((kdn.kdn_fp8_matmul(*one, *one) == 0).all())
     with pytest.raises(ValueError):
         kdn.kdn_fp8_matmul(*a, b[0], b[1][:3])
+
+
+@pytest.mark.parametrize("out", [F32, BF16])
+@pytest.mark.parametrize("tile", [False, True])
+@pytest.mark.parametrize("M,N,K", [(5, 100, 200), (17, 129, 384), (40, 333, 200), (300, 333, 200),
+                                   (700, 1000, 260), (1300, 1403, 200), (2100, 2312, 130),
+                                   (4000, 2047, 260)])
+def test_matmul_writes_nothing_around_its_output(M, N, K, tile, out):
+    """Few rows and tiles of both widths, rows that bulk copies store and rows that
+    they cannot; several tiles a pair."""
+    g = torch.Generator().manual_seed(M + N)
+    x = kdn.kdn_fp8_quantize(torch.randn(M, K, generator=g).cuda())
+    w = kdn.kdn_fp8_quantize(torch.randn(N, K, generator=g).cuda(), tile=tile)
+    want = kdn.kdn_fp8_matmul(*x, *w, out_dtype=out)
+    room = torch.full((M + 16, N), 3.0, dtype=out, device='cuda')
+    got = kdn.kdn_fp8_matmul(*x, *w, out_dtype=out, out=room[8:8 + M])
+    assert torch.equal(got, want)
+    assert bool((room[:8] == 3).all()) and bool((room[8 + M:] == 3).all())
+    v = [f64(q.float()) * fp8_ref.spread(f64(s), *q.shape, t) for q, s, t in ((*x, False), (*w, tile))]
+    exact, size = v[0] @ v[1].T, np.abs(v[0]) @ np.abs(v[1]).T
+    # (a block's 128 additions at 2^-23, three for each block, and the output's own)
+    tol = (128 + 3 * -(-K // 128) + 8) * 2.0 ** -23 * size
+    tol = tol + (2.0 ** -24 if out is F32 else 2.0 ** -8) * (np.abs(exact) + tol)
+    assert (np.abs(f64(got) - exact) <= tol).all()
