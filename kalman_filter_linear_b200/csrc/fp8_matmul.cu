@@ -37,6 +37,7 @@
 
 #include <atomic>
 
+#include "enqueue.h"
 #include "kdn_common.cuh"
 
 namespace kdn {

@@ -16,6 +16,7 @@
 // the row XORed by the piece's column, which keeps the column-wise stores free
 // of bank conflicts, and leave as 16-byte stores.  32749 x 1000 in bf16, turned:
 // 19.7 us (5.0 TB/s).
+#include "enqueue.h"
 #include "fp8_common.cuh"
 
 namespace kdn {

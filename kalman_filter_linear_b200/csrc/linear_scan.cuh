@@ -30,6 +30,7 @@
 // sequence stays out of the next (products that are zero get the sign +).
 #pragma once
 
+#include "enqueue.h"
 #include "kdn_common.cuh"
 
 namespace kdn {

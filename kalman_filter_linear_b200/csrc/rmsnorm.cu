@@ -22,6 +22,7 @@
 // consecutive, and a block of 128 is a warp's.
 #include <atomic>
 
+#include "enqueue.h"
 #include "fp8_common.cuh"
 
 namespace kdn {
