@@ -61,22 +61,33 @@ def build(verbose=False, extra=()):
     return LIB
 
 
-def build_quick(verbose=False):
-    """Compile _kdn_quick.so; without it the binding works the same, slower."""
+def quick_sources():
+    return [os.path.join(PKG, 'csrc', 'quick_binding.cpp'), os.path.join(ROOT, 'include', 'kdn.h')]
+
+
+def quick_command():
+    """The command that compiles _kdn_quick.so, or None without torch or g++."""
     spec = importlib.util.find_spec('torch')
     cxx = shutil.which('g++')
-    if os.path.exists(QUICK):
-        os.remove(QUICK)
     if spec is None or cxx is None:
-        return
+        return None
     torch = os.path.dirname(spec.origin)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
-    cmd = [cxx, '-O2', '-std=c++17', '-fPIC', '-shared', '-I', os.path.join(torch, 'include'),
-           '-I', os.path.join(torch, 'include', 'torch', 'csrc', 'api', 'include'),
-           '-I', os.path.join(cuda, 'include'), '-I', sysconfig.get_paths()['include'],
-           os.path.join(PKG, 'csrc', 'quick_binding.cpp'), '-o', QUICK + '.tmp', '-L', PKG,
-           '-l:libkdn.so', '-L', os.path.join(torch, 'lib'), '-lc10', '-lc10_cuda', '-ltorch',
-           '-ltorch_cpu', '-ltorch_python', '-Wl,-rpath,$ORIGIN']
+    return [cxx, '-O2', '-std=c++17', '-fPIC', '-shared', '-I', os.path.join(torch, 'include'),
+            '-I', os.path.join(torch, 'include', 'torch', 'csrc', 'api', 'include'),
+            '-I', os.path.join(cuda, 'include'), '-I', sysconfig.get_paths()['include'],
+            quick_sources()[0], '-o', QUICK + '.tmp', '-L', PKG,
+            '-l:libkdn.so', '-L', os.path.join(torch, 'lib'), '-lc10', '-lc10_cuda', '-ltorch',
+            '-ltorch_cpu', '-ltorch_python', '-Wl,-rpath,$ORIGIN']
+
+
+def build_quick(verbose=False):
+    """Compile _kdn_quick.so; without it the binding works the same, slower."""
+    cmd = quick_command()
+    if os.path.exists(QUICK):
+        os.remove(QUICK)
+    if cmd is None:
+        return
     if verbose:
         print(' '.join(cmd), flush=True)
     if subprocess.run(cmd).returncode == 0:
@@ -85,13 +96,21 @@ def build_quick(verbose=False):
         print('_kdn_quick.so could not be built: calls go through ctypes', file=sys.stderr)
 
 
+def quick_is_stale():
+    """Whether _kdn_quick.so is missing or older than its sources, and could be built."""
+    if os.path.exists(QUICK) and \
+            os.path.getmtime(QUICK) >= max(os.path.getmtime(d) for d in quick_sources()):
+        return False
+    return quick_command() is not None
+
+
 def is_stale():
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(PKG, 'csrc', '*.cpp')) + glob.glob(os.path.join(PKG, 'csrc', '*.cuh')) + \
+    deps = sources() + glob.glob(os.path.join(PKG, 'csrc', '*.cuh')) + \
         glob.glob(os.path.join(PKG, 'csrc', '*.h')) + glob.glob(os.path.join(ROOT, 'include', '*.h'))
-    return any(os.path.getmtime(d) > t for d in deps)
+    return any(os.path.getmtime(d) > t for d in deps) or quick_is_stale()
 
 
 if __name__ == '__main__':

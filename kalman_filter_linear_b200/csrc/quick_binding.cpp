@@ -13,6 +13,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include "../../include/kdn.h"
 
@@ -353,4 +354,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kdn_quick", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__kdn_quick() { return PyModule_Create(&module); }
+// (kdn.py leaves a module that was built against another torch unused)
+PyMODINIT_FUNC PyInit__kdn_quick() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) < 0) Py_CLEAR(m);
+  return m;
+}

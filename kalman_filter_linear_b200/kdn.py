@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import warnings
 
 import torch
 
@@ -565,8 +566,16 @@ def _load_quick():
     lib()
     try:
         from . import _kdn_quick
+        why = None if _kdn_quick.torch_version == torch.__version__.partition('+')[0] else \
+            f'it was built against torch {_kdn_quick.torch_version}'
+    except ImportError as e:
+        why = e
+    if why is None:
         _quick = _kdn_quick
-    except ImportError:
+    else:
+        warnings.warn(f'_kdn_quick.so is not used ({why}): small calls take about twice as long. '
+                      '`python -m kalman_filter_linear_b200.build` builds it', RuntimeWarning,
+                      stacklevel=3)
         _quick = _NoQuick
     return _quick
 
