@@ -65,6 +65,30 @@ kdn_status kdn_testing_kla_skip_v_copy(const void* q, const void* k,
                                        void* workspace, size_t workspace_bytes,
                                        void* stream);
 
+/* kdn_linear_scan_forward (fp32, no write gate, h0 = 0; more than two columns
+ * of 64 channels, which stream), except that the first block's copy of its tile
+ * `skip_tile` is never issued.  The bounded waits for it, and for the maps that
+ * depend on it, give up (after about a second) and record KDN_ERR_TIMEOUT in
+ * the workspace error word; every role leaves through its bounded waits, waits
+ * (bounded) for copies and maps on their way to its block, and returns.
+ * Outputs are not meaningful.  skip_tile >= 0; T >= 8. */
+kdn_status kdn_testing_linear_scan_skip_copy(const float* a, const float* x,
+                                             float* y, float* h_out, int B,
+                                             int T, int D, int64_t skip_tile,
+                                             void* workspace,
+                                             size_t workspace_bytes,
+                                             void* stream);
+
+/* kdn_fp8_matmul (M >= 1), except that the first block's copies of its block
+ * `skip_block` along K are never issued.  The waits for them give up as above,
+ * and KDN_ERR_TIMEOUT is recorded in `status`.  Outputs are not meaningful.
+ * skip_block >= 0. */
+kdn_status kdn_testing_fp8_matmul_skip_copy(
+    const void* x, int64_t ldx, const float* x_scale, const void* w,
+    int64_t ldw, const float* w_scale, int w_tile, void* out,
+    kdn_dtype out_dtype, int M, int N, int K, int skip_block,
+    uint32_t* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -216,6 +216,7 @@ struct Prm {
   int M, N, kbs;         // rows of x, rows of w, blocks along k
   bool bulk_out;         // out's rows are 16-byte pieces: bulk copies store them
   uint32_t* status;      // or null
+  uint32_t skip;         // for tests: the first block's copies that are left out, or ~0
 };
 
 // ------------------------------------------------------------------- wide
@@ -300,6 +301,7 @@ fp8_matmul_wide(const __grid_constant__ CUtensorMap mx, const __grid_constant__ 
     if (warp == 0 && lane == 0) {
       // copies
       uint32_t it = 0;
+      const uint32_t skip = blockIdx.x == 0 ? p.skip : ~0u;
       bool bad = false;
       for (int tile = pair; tile < tiles && !bad; tile += pairs) {
         const int m0 = tile / tiles_n * 256 + (int)rank * 128;
@@ -308,6 +310,7 @@ fp8_matmul_wide(const __grid_constant__ CUtensorMap mx, const __grid_constant__ 
           const uint32_t st = it % S;
           if (it >= (uint32_t)S && fail(&empty[st], ((it / S) - 1u) & 1u)) { bad = true; break; }
           if (rank == 0) mbar_expect_tx(&full[st], 2 * W::STAGE);
+          if (it == skip) continue;
           const uint32_t bar = at_rank(&full[st], 0);
           tma_load_pair(sbase + st * W::STAGE, &mx, bar, kb * (int)kKb, m0);
           tma_load_pair(sbase + st * W::STAGE + W::A, &mw, bar, kb * (int)kKb, n0);
@@ -433,7 +436,11 @@ fp8_matmul_wide(const __grid_constant__ CUtensorMap mx, const __grid_constant__ 
       const float* sc = nullptr;
       for (int kb = 0, k = 0; kb < p.kbs; ++kb) {
         if (k == 0) {
-          if (warp_fail(&sc_full[g & 1u], (g >> 1) & 1u)) { bad = true; break; }
+          if (warp_fail(&sc_full[g & 1u], (g >> 1) & 1u)) {
+            tmem_ld_wait(r[0]);  // (nothing may arrive in registers that are used again)
+            bad = true;
+            break;
+          }
           sc = scales + (g & 1u) * (W::SC / 4);
         }
         float s[TILE ? 1 : 4];
@@ -672,17 +679,19 @@ fp8_matmul_few(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
 #pragma unroll
   for (int i = 0; i < BT / 2; ++i) acc[i] = make_float2(0.f, 0.f);
   if (warp == 0 && lane == 0) {
-    bool bad = false;
+    const uint32_t skip = blockIdx.x == 0 ? p.skip : ~0u;
     int it = 0;
     for (; it < nk; ++it) {
       const int st = it % S;
-      if (it >= S && fail(&empty[st], (uint32_t)((it / S) - 1) & 1u)) { bad = true; break; }
+      if (it >= S && fail(&empty[st], (uint32_t)((it / S) - 1) & 1u)) break;
       mbar_expect_tx(&full[st], F::STAGE);
+      if ((uint32_t)it == skip) continue;
       tma_load_2d(sbase + st * F::STAGE, &mw, &full[st], (k0 + it) * (int)kKb, n0);
       tma_load_2d(sbase + st * F::STAGE + F::A, &mx, &full[st], (k0 + it) * (int)kKb, m0);
     }
-    if (bad)
-      for (int i = it > S ? it - S : 0; i < it; ++i) mbar_wait(&full[i % S], (uint32_t)(i / S) & 1u);
+    // copies in flight land before their place is used again, whatever became of
+    // the other warps (bounded)
+    for (int i = it > S ? it - S : 0; i < it; ++i) mbar_wait(&full[i % S], (uint32_t)(i / S) & 1u);
   } else if (warp == 1 && lane == 0) {
     constexpr uint32_t ID = umma_idesc_e4m3(128, BT);
     int it = 0;
@@ -945,7 +954,7 @@ kdn_status mm_go(const void* x, int64_t ldx, const void* w, int64_t ldw, int K, 
 
 kdn_status fp8_matmul_launch(const void* x, int64_t ldx, const float* sx, const void* w,
                              int64_t ldw, const float* sw, bool tile, void* out, kdn_dtype ot,
-                             int M, int N, int K, uint32_t* status, cudaStream_t s) {
+                             int M, int N, int K, uint32_t* status, cudaStream_t s, uint32_t skip) {
   int dev = 0;
   static std::atomic<int> sm_count[64];
   if (cudaGetDevice(&dev) != cudaSuccess) return KDN_ERR_CUDA;
@@ -955,7 +964,7 @@ kdn_status fp8_matmul_launch(const void* x, int64_t ldx, const float* sx, const 
       return KDN_ERR_CUDA;
     sm_count[dev & 63].store(sms, std::memory_order_relaxed);
   }
-  Prm p{sx, sw, out, M, N, (int)(((int64_t)K + kKb - 1) / kKb), false, status};
+  Prm p{sx, sw, out, M, N, (int)(((int64_t)K + kKb - 1) / kKb), false, status, skip};
   using bf = __nv_bfloat16;
   if (ot == KDN_F32)
     return tile ? mm_go<true, float>(x, ldx, w, ldw, K, p, dev, sms, s)

@@ -65,7 +65,7 @@ size_t linear_scan_workspace_size(int B, int T, int D);
 kdn_status linear_scan_forward_launch(const void* a, const void* b, kdn_dtype gate_dtype,
                                       const void* x, kdn_dtype in_dtype, const float* h0, void* y,
                                       float* h_out, const int32_t* cu, int N, int B, int T, int D,
-                                      void* workspace, cudaStream_t s);
+                                      void* workspace, cudaStream_t s, int64_t skip = -1);
 kdn_status linear_scan_step_launch(const void* a, const void* b, kdn_dtype gate_dtype,
                                    const void* x, kdn_dtype in_dtype, float* h, void* y, int64_t n,
                                    cudaStream_t s);
@@ -88,7 +88,8 @@ kdn_status fp8_quantize_launch(const void* x, kdn_dtype xt, void* q, int64_t ldq
                                cudaStream_t s);
 kdn_status fp8_matmul_launch(const void* x, int64_t ldx, const float* sx, const void* w,
                              int64_t ldw, const float* sw, bool tile, void* out, kdn_dtype ot,
-                             int M, int N, int K, uint32_t* status, cudaStream_t s);
+                             int M, int N, int K, uint32_t* status, cudaStream_t s,
+                             uint32_t skip = ~0u);
 }  // namespace kdn
 
 namespace {
@@ -734,10 +735,10 @@ kdn_status kdn_fp8_quantize(const void* x, kdn_dtype x_dtype, int64_t rows, int6
                                   as_stream(stream));
 }
 
-kdn_status kdn_fp8_matmul(const void* x, int64_t ldx, const float* x_scale, const void* w,
-                          int64_t ldw, const float* w_scale, int w_tile, void* out,
-                          kdn_dtype out_dtype, int M, int N, int K, uint32_t* status,
-                          void* stream) {
+namespace {
+kdn_status matmul_args(const void* x, int64_t ldx, const float* x_scale, const void* w, int64_t ldw,
+                       const float* w_scale, void* out, kdn_dtype out_dtype, int M, int N, int K,
+                       const uint32_t* status) {
   if (!x || !x_scale || !w || !w_scale || !out) return KDN_ERR_INVALID_ARG;
   if (!f32_or_bf16(out_dtype) || M < 0 || N < 1 || K < 1) return KDN_ERR_INVALID_ARG;
   if (!fp8_matrix(x, ldx, K) || !fp8_matrix(w, ldw, K) || !al16(out)) return KDN_ERR_INVALID_ARG;
@@ -748,9 +749,50 @@ kdn_status kdn_fp8_matmul(const void* x, int64_t ldx, const float* x_scale, cons
   if (M > 0x7fffff00 || N > 0x7fffff00 || K > 0x7fffff00 ||
       ((int64_t)M + 15) / 16 * (((int64_t)N + 127) / 128) * 8 > 0x7fffffffll)
     return KDN_ERR_UNSUPPORTED;
+  return KDN_OK;
+}
+}  // namespace
+
+kdn_status kdn_fp8_matmul(const void* x, int64_t ldx, const float* x_scale, const void* w,
+                          int64_t ldw, const float* w_scale, int w_tile, void* out,
+                          kdn_dtype out_dtype, int M, int N, int K, uint32_t* status,
+                          void* stream) {
+  const kdn_status st = matmul_args(x, ldx, x_scale, w, ldw, w_scale, out, out_dtype, M, N, K,
+                                    status);
+  if (st != KDN_OK) return st;
   if (M == 0) return KDN_OK;
   return kdn::fp8_matmul_launch(x, ldx, x_scale, w, ldw, w_scale, w_tile != 0, out, out_dtype, M,
                                 N, K, status, as_stream(stream));
+}
+
+kdn_status kdn_testing_linear_scan_skip_copy(const float* a, const float* x, float* y,
+                                             float* h_out, int B, int T, int D, int64_t skip_tile,
+                                             void* workspace, size_t workspace_bytes,
+                                             void* stream) {
+  if (!a || !x || !y || !h_out || skip_tile < 0) return KDN_ERR_INVALID_ARG;
+  if (!al16(a) || !al16(x) || !al16(y) || !al16(h_out)) return KDN_ERR_INVALID_ARG;
+  kdn_status st = scan_shape(nullptr, B, T, D);
+  if (st != KDN_OK) return st;
+  // (more than two columns of 64 channels always stream)
+  if (T < 8 || (int64_t)B * ((D + 63) / 64) <= 2) return KDN_ERR_INVALID_ARG;
+  st = scan_workspace(workspace, workspace_bytes, B, T, D);
+  if (st != KDN_OK) return st;
+  return kdn::linear_scan_forward_launch(a, nullptr, KDN_F32, x, KDN_F32, nullptr, y, h_out,
+                                         nullptr, B, B, T, D, workspace, as_stream(stream),
+                                         skip_tile);
+}
+
+kdn_status kdn_testing_fp8_matmul_skip_copy(const void* x, int64_t ldx, const float* x_scale,
+                                            const void* w, int64_t ldw, const float* w_scale,
+                                            int w_tile, void* out, kdn_dtype out_dtype, int M,
+                                            int N, int K, int skip_block, uint32_t* status,
+                                            void* stream) {
+  if (skip_block < 0 || M < 1) return KDN_ERR_INVALID_ARG;
+  const kdn_status st = matmul_args(x, ldx, x_scale, w, ldw, w_scale, out, out_dtype, M, N, K,
+                                    status);
+  if (st != KDN_OK) return st;
+  return kdn::fp8_matmul_launch(x, ldx, x_scale, w, ldw, w_scale, w_tile != 0, out, out_dtype, M,
+                                N, K, status, as_stream(stream), (uint32_t)skip_block);
 }
 
 kdn_status kdn_read_workspace_status(const void* workspace, size_t workspace_bytes,

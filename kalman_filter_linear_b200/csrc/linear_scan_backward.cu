@@ -230,6 +230,7 @@ kdn_status linear_scan_backward_launch(const void* a, const void* b, kdn_dtype g
   k.D = D;
   k.workspace = workspace;
   k.stream = s;
+  k.skip = -1;
   kdn_status st = KDN_OK;
   if (D % 8 == 0 ? ls_stream_call<true, true>(k, &st) : ls_stream_call<true, false>(k, &st))
     return st;

@@ -22,6 +22,7 @@ struct LsCall {
   int N, B, T, D;
   void* workspace;
   cudaStream_t stream;
+  int64_t skip;               // streaming form, for tests: the first block's copy that is left out, or -1
 };
 
 // Runs a call in its streaming form, EIGHT for a D that is a multiple of 8; or

@@ -232,7 +232,7 @@ size_t linear_scan_workspace_size(int B, int T, int D) {
 kdn_status linear_scan_forward_launch(const void* a, const void* b, kdn_dtype gate_dtype,
                                       const void* x, kdn_dtype in_dtype, const float* h0, void* y,
                                       float* h_out, const int32_t* cu, int N, int B, int T, int D,
-                                      void* workspace, cudaStream_t s) {
+                                      void* workspace, cudaStream_t s, int64_t skip) {
   LsCall k{};
   k.a = a;
   k.b = b;
@@ -249,6 +249,7 @@ kdn_status linear_scan_forward_launch(const void* a, const void* b, kdn_dtype ga
   k.D = D;
   k.workspace = workspace;
   k.stream = s;
+  k.skip = skip;
   kdn_status st = KDN_OK;
   if (D % 8 == 0 ? ls_stream_call<false, true>(k, &st) : ls_stream_call<false, false>(k, &st))
     return st;

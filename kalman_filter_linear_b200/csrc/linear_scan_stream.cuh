@@ -76,6 +76,7 @@ struct LsArgs {
   int64_t lines8;                // not EIGHT: rows of all entries that are in whole lines of 8
   const void* in[5];             // not EIGHT: the tensors of the maps, for the rows behind them
   uint32_t* error;
+  int64_t skip;                  // (LsCall)
 };
 
 template <bool BWD, typename GT, typename XT, bool HAS_B, bool EIGHT>
@@ -312,6 +313,7 @@ linear_scan_stream_kernel(const __grid_constant__ CUtensorMap ma, const __grid_c
     int st = 0;
     uint32_t phase = 1;
     Pos q{col0, 0};
+    const int64_t skip = blockIdx.x == 0 ? p.skip : -1;
     // (one lane where it issues alone: a vote of the warp each time costs 6 %)
     for (; n < total && (!EIGHT || lane == 0); ++n, next(q, 1)) {
       const bool bad = n >= NS && lane == 0 && fail(&empty[st], phase);
@@ -325,7 +327,8 @@ linear_scan_stream_kernel(const __grid_constant__ CUtensorMap ma, const __grid_c
         if (lane == 0) mbar_expect_tx(&full[st], S::SENT);
         if (!EIGHT) __syncwarp();
         auto copy = [&](uint32_t at, const CUtensorMap& m, int back, int es, uint32_t box) {
-          ls_copy<EIGHT>(d + at, &m, &full[st], c0, t - back, bi, R - back, p.D, es, box, lane);
+          if (n != skip)
+            ls_copy<EIGHT>(d + at, &m, &full[st], c0, t - back, bi, R - back, p.D, es, box, lane);
         };
         copy(S::A, ma, 0, S::G, S::BG * S::G);
         copy(S::X0, mx, 0, S::X, S::BX * S::X);
@@ -377,7 +380,8 @@ linear_scan_stream_kernel(const __grid_constant__ CUtensorMap ma, const __grid_c
     };
     Pos q{col0, 0};
     float2 state = make_float2(0.f, 0.f), later = enter(col0);
-    for (int64_t n = 0; n < total; ++n, next(q, 1)) {
+    int64_t n = 0;
+    for (; n < total; ++n, next(q, 1)) {
       const int g = (int)(n % G), sl = (int)(n % W);
       if (q.wave == 0) {
         state = later;
@@ -399,6 +403,11 @@ linear_scan_stream_kernel(const __grid_constant__ CUtensorMap ma, const __grid_c
       __syncwarp();
       if (lane == 0) mbar_arrive(&carried[g]);
     }
+    // Where this gave up, maps that the other CTAs have sent land before the CTA's
+    // memory goes (bounded; they cannot send more than the slots hold).
+    if (lane == 0)
+      for (int64_t i = n; i < total && i < n + W; ++i)
+        if (!mbar_wait(&maps_full[i % W], (uint32_t)(i / W) & 1u)) break;
   } else {
     // ------------------------------------------------------------- steps
     const int g = warp >> 2, w4 = warp & 3;
@@ -857,6 +866,7 @@ bool ls_stream_types(const LsCall& k, kdn_status* st) {
   p.N = k.N;
   p.T = k.T;
   p.D = k.D;
+  p.skip = k.skip;
   const void *x = BWD ? k.dy : k.x, *x1 = BWD ? k.x : nullptr;
   *st = packed ? ls_stream_go<BWD, GT, XT, HAS_B, true, EIGHT>(k.a, x, k.y, k.b, x1, p, k.B, same,
                                                                k.workspace, k.stream)

@@ -119,6 +119,11 @@ def lib():
     L.kdn_testing_mobius_scan_unpublished_tile.restype = _i32
     L.kdn_testing_kla_skip_v_copy.restype = _i32
     L.kdn_testing_kla_skip_v_copy.argtypes = [_vp] * 9 + [_i32] * 4 + [_vp, _sz, _vp]
+    L.kdn_testing_linear_scan_skip_copy.restype = _i32
+    L.kdn_testing_linear_scan_skip_copy.argtypes = [_vp] * 4 + [_i32] * 3 + [_i64, _vp, _sz, _vp]
+    L.kdn_testing_fp8_matmul_skip_copy.restype = _i32
+    L.kdn_testing_fp8_matmul_skip_copy.argtypes = [_vp, _i64, _vp, _vp, _i64, _vp, _i32, _vp] + \
+        [_i32] * 5 + [_vp, _vp]
     L.kdn_testing_forward_skip_v_copy.restype = _i32
     L.kdn_testing_forward_skip_v_copy.argtypes = [_i32] + [_vp] * 9 + [_i32] * 4 + [_vp, _sz, _vp]
     L.kdn_testing_mobius_scan_unpublished_tile.argtypes = [_vp] * 5 + [_f32, _vp, _i64, _i64,
@@ -1012,3 +1017,34 @@ def kdn_testing_kla_skip_v_copy(q, k, v, a, w, r, skip_chunk, workspace):
                                            _ptr(workspace), workspace.numel(), _stream())
     _check(st, 'kdn_testing_kla_skip_v_copy')
     return o, S, lam
+
+
+def kdn_testing_linear_scan_skip_copy(a, x, skip_tile, workspace):
+    """Fault-injection hook: the streamed recurrence (fp32) with one copy of the
+    first block left out.  Returns (y, h_T); the status is in the workspace."""
+    B, T, D = a.shape
+    for t, n in ((a, 'a'), (x, 'x')):
+        _req(t, n, torch.float32, (B, T, D))
+    _req(workspace, 'workspace', torch.uint8)
+    y, h = torch.empty_like(x), torch.empty((B, D), dtype=torch.float32, device=x.device)
+    st = lib().kdn_testing_linear_scan_skip_copy(_ptr(a), _ptr(x), _ptr(y), _ptr(h), B, T, D,
+                                                 int(skip_tile), _ptr(workspace),
+                                                 workspace.numel(), _stream())
+    _check(st, 'kdn_testing_linear_scan_skip_copy')
+    return y, h
+
+
+def kdn_testing_fp8_matmul_skip_copy(x, x_scale, w, w_scale, skip_block, status):
+    """Fault-injection hook: kdn_fp8_matmul with the first block's copies of one
+    block along K left out.  Returns the product (fp32); `status` is one zeroed
+    int32 word."""
+    (M, K), N = x.shape, w.shape[0]
+    px, ldx = _fp8_arg(x, 'x', M, K, x.device)
+    pw, ldw = _fp8_arg(w, 'w', N, K, x.device)
+    _req(status, 'status', torch.int32, (1,))
+    out = torch.empty((M, N), dtype=torch.float32, device=x.device)
+    st = lib().kdn_testing_fp8_matmul_skip_copy(
+        px, ldx, _ptr(x_scale), pw, ldw, _ptr(w_scale), int(w_scale.shape[0] != N), _ptr(out),
+        KDN_F32, M, N, K, int(skip_block), _ptr(status), _stream())
+    _check(st, 'kdn_testing_fp8_matmul_skip_copy')
+    return out
