@@ -683,7 +683,9 @@ def kdn_linear_scan_forward(a, x, b=None, h0=None, cu_seqlens=None, y=None, h_ou
     [B, T, D], or [T, D] with cu_seqlens [B + 1] int32 (packed sequences);
     a and b share a dtype (fp32 or bf16), h0 [B, D] fp32.  Returns (y like x,
     h_T [B, D] fp32).  With cu_seqlens, the rows of y behind the last sequence
-    are left as they were."""
+    are left as they were.  Offsets out of order and a wait that gave up are told
+    by kdn_read_workspace_status(workspace), so only where a workspace is given;
+    without one such a call returns unspecified values."""
     if workspace is None:
         r = (_quick or _load_quick()).scan_forward(a, x, b, h0, cu_seqlens, y, h_out)
         if r is not None:
@@ -713,7 +715,8 @@ def kdn_linear_scan_backward(a, x, y, dy, b=None, h0=None, dh_T=None, cu_seqlens
                              dx=None, db=None, dh0=None, workspace=None):
     """The gradients of kdn_linear_scan_forward, given its output y, dy like y
     and dh_T [B, D] fp32 (or None): a dict of a, x, h0 (fp32) and, when b is
-    given, b.  x is read only with b, and may be None without."""
+    given, b.  x is read only with b, and may be None without.  The status is in a
+    given workspace, as the forward's."""
     if workspace is None:
         r = (_quick or _load_quick()).scan_backward(a, x, y, dy, b, h0, dh_T, cu_seqlens, da, dx, db,
                                                     dh0)
@@ -925,7 +928,8 @@ def kdn_fp8_matmul(x, x_scale, w, w_scale, out_dtype=torch.bfloat16, out=None, s
     16-byte boundaries, as kdn_fp8_quantize lays them out), x_scale
     [M, ceil(K / 128)], w_scale [ceil(N / 128), ceil(K / 128)] (128 x 128
     tiles) or [N, ceil(K / 128)], fp32.  Returns [M, N] in out_dtype (bfloat16
-    or float32): zeros for K = 0.  status: one zeroed int32 word that a timed-out wait sets."""
+    or float32): zeros for K = 0.  status: one zeroed int32 word that a timed-out
+    wait sets (kdn_read_workspace_status); without one it is not told."""
     r = (_quick or _load_quick()).matmul(x, x_scale, w, w_scale, _CODE.get(out_dtype, -1), out, status)
     if r is not None:
         return r
