@@ -17,11 +17,11 @@
 // four warps cover the 128 rows (TMEM lanes), each group half the columns.
 // Scaled sums leave through shared memory in bulk copies.
 //
-// 32768 x 2048 x 2048 takes 130 us (2.1 PFLOP/s), 2048 x 2048 x 32749 with a
-// scale for each row of w 200.  The loop without scaling takes 87 us, at the 1.25
-// to 1.4 GHz that the power limit leaves; with the hand-over of TMEM 96, with
-// its reads still 96, with the multiply-adds 125: a warp's own chain of read,
-// scale, add and release bounds it.  Handing TMEM over in parts of 128 columns
+// 32768 x 2048 x 2048 takes 136 us (2.0 PFLOP/s; 157 at the 1.5 GHz that the power
+// limit leaves after a second of such work), 2048 x 2048 x 32749 with a scale for
+// each row of w 209.  Of 130 us in the same run, the loop without scaling took 87;
+// with the hand-over of TMEM 96, with its reads still 96, with the multiply-adds
+// 125: a warp's own chain of read, scale, add and release bounds it.  Handing TMEM over in parts of 128 columns
 // (145), sixteen scaling warps (143) and 128-column tiles with four accumulators
 // (152) were no faster.
 //
@@ -29,7 +29,7 @@
 // 128-row operand and up to 64 rows of x are the columns; the blocks of k are
 // split over a cluster of up to eight CTAs so that every SM streams w, and the
 // parts meet through distributed shared memory, added in rank order.  8 x 2048 x
-// 2048 takes 5.6 us, 8 x 8192 x 8192 12.6 (5.3 TB/s).
+// 2048 takes 5.8 us, 8 x 8192 x 8192 16 (4.2 TB/s; 12 where w is still in L2).
 //
 // Every wait is bounded; one that gives up sets the status word.
 #include <cuda.h>

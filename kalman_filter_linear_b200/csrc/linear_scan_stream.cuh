@@ -12,8 +12,8 @@
 // does not depend on timing.  (A look-back through global memory, in place of
 // the cluster, took 231 us for 8 x 4096 x 2048 with fp32 gates and 1034 us for
 // 65536 x 2048: a tile held its shared memory for the three to five L2 round
-// trips that a look-back takes.)  These take 85 and 183 us (6.3 and 5.9 TB/s),
-// the packed backward pass over 32768 x 2048 with fp32 gates 262 (6.1 TB/s):
+// trips that a look-back takes.)  These take 85 and 186 us (6.3 and 5.8 TB/s),
+// the packed backward pass over 32768 x 2048 with fp32 gates 253 (6.4 TB/s):
 // HBM bounds them.
 //
 // Warps of a CTA: one copies inputs (bulk tensor copies) into a ring of stages;

@@ -12,8 +12,8 @@
 // registers between its reduction and its use, and the next row's loads are
 // under way meanwhile.  Rows are taken in turn by as many blocks as stay on the
 // device at once, eight elements a thread up to rows of 4096: 32768 rows of
-// 2048, fp32 with a bf16 stream to e4m3, take 90 us (6.7 TB/s), backward 128
-// (6.3 TB/s); a warp a row with 64 elements a lane, loaded as its turn came,
+// 2048, fp32 with a bf16 stream to e4m3, take 94 us (6.4 TB/s), backward 131
+// (6.2 TB/s); a warp a row with 64 elements a lane, loaded as its turn came,
 // took 268 and 309.  A row has G threads.
 // VEC (rows of a multiple of 8): thread t holds the elements [8 (t + G v),
 // 8 (t + G v) + 8), so loads are 16 bytes a thread and a block of 128 is a half
