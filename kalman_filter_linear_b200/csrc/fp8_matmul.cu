@@ -32,11 +32,9 @@
 // 2048 takes 5.8 us, 8 x 8192 x 8192 16 (4.2 TB/s; 12 where w is still in L2).
 //
 // Every wait is bounded; one that gives up sets the status word.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include <atomic>
 
+#include "cluster.cuh"
 #include "enqueue.h"
 #include "kdn_common.cuh"
 
@@ -129,15 +127,6 @@ __device__ __forceinline__ float2 as_f2(uint32_t a, uint32_t b) {
   return make_float2(__uint_as_float(a), __uint_as_float(b));
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 // the address of `p` in CTA `rank`'s shared memory
 __device__ __forceinline__ uint32_t at_rank(const void* p, uint32_t rank) {
   uint32_t a;
@@ -811,26 +800,10 @@ fp8_matmul_few(const __grid_constant__ CUtensorMap mx, const __grid_constant__ C
 }
 
 // ------------------------------------------------------------------- host
-PFN_cuTensorMapEncodeTiled_v12000 mm_encoder() {
-  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> fn{nullptr};
-  PFN_cuTensorMapEncodeTiled_v12000 f = fn.load(std::memory_order_acquire);
-  if (!f) {
-    void* q = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &q, 12000, cudaEnableDefault,
-                                         &found) != cudaSuccess ||
-        found != cudaDriverEntryPointSuccess)
-      return nullptr;
-    f = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(q);
-    fn.store(f, std::memory_order_release);
-  }
-  return f;
-}
-
 // [rows, K] bytes, rows ld bytes apart, boxes of 128 bytes x box rows; what
 // lies outside reads as zero.
 bool mm_map(CUtensorMap* m, const void* base, int rows, int K, int64_t ld, int box) {
-  auto enc = mm_encoder();
+  auto enc = tensor_map_encoder();
   if (!enc) return false;
   cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)ld};
@@ -844,7 +817,7 @@ bool mm_map(CUtensorMap* m, const void* base, int rows, int K, int64_t ld, int b
 
 // out [M, N], boxes of 32 rows x 128 bytes
 bool mm_out_map(CUtensorMap* m, void* out, int M, int N, size_t es) {
-  auto enc = mm_encoder();
+  auto enc = tensor_map_encoder();
   if (!enc) return false;
   cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)M};
   cuuint64_t strides[1] = {(cuuint64_t)N * es};

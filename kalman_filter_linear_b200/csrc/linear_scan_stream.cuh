@@ -45,13 +45,11 @@
 // box; the warps fetch them.
 #pragma once
 
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include <atomic>
 #include <cstring>
 #include <type_traits>
 
+#include "cluster.cuh"
 #include "linear_scan.cuh"
 #include "linear_scan_call.h"
 
@@ -201,20 +199,6 @@ __device__ __forceinline__ void ls_boundaries(const int32_t* cu, int N, int t0, 
   fin = __reduce_or_sync(0xffffffffu, e);
 }
 
-__device__ __forceinline__ uint32_t ls_cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t ls_cluster_size() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void ls_cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 // 16 bytes into the same place of CTA `rank`'s shared memory, counted by its
 // barrier
 __device__ __forceinline__ void ls_send(const void* at, uint64_t* bar, uint32_t rank, float4 v) {
@@ -245,7 +229,7 @@ linear_scan_stream_kernel(const __grid_constant__ CUtensorMap ma, const __grid_c
   __shared__ uint32_t abort_word;
   uint8_t* sm = stream_raw + ((128u - (smem_u32(stream_raw) & 127u)) & 127u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = (int)ls_cluster_rank(), C = (int)ls_cluster_size();
+  const int rank = (int)cluster_rank(), C = (int)cluster_size();
   // this cluster's columns: col0, col0 + ncl, ...; a wave is C tiles of one
   const int ncl = (int)gridDim.x / C, col0 = (int)blockIdx.x / C;
   const int waves = (p.chunks + C - 1) / C;
@@ -282,7 +266,7 @@ linear_scan_stream_kernel(const __grid_constant__ CUtensorMap ma, const __grid_c
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncwarp();
-  ls_cluster_sync();
+  cluster_sync_all();
 
   // (at least 0, so that no difference with a step overflows)
   const int end = PACKED ? max(0, min(p.T, __ldg(p.cu + p.N))) : p.T;
@@ -720,29 +704,16 @@ linear_scan_stream_kernel(const __grid_constant__ CUtensorMap ma, const __grid_c
   }
   // no CTA's shared memory goes while another may still write to it
   __syncwarp();
-  ls_cluster_sync();
+  cluster_sync_all();
 }
 
 // ------------------------------------------------------------------- host
-inline PFN_cuTensorMapEncodeTiled_v12000 ls_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
-    void* q = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &q, 12000, cudaEnableDefault,
-                                         &found) != cudaSuccess ||
-        found != cudaDriverEntryPointSuccess)
-      return nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(q);
-  }();
-  return fn;
-}
-
 // EIGHT: [entries, T, D] of 2- or 4-byte elements, boxes of 64 channels x the
 // tile's steps; else lines of eight rows of D, boxes of one row a line.
 template <bool EIGHT>
 bool ls_map(CUtensorMap* m, const void* base, int es, int64_t entries, int64_t T, int64_t D,
             int wide, int box_rows) {
-  auto enc = ls_encoder();
+  auto enc = tensor_map_encoder();
   if (!enc) return false;
   cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)T, (cuuint64_t)entries};
   cuuint64_t strides[2] = {(cuuint64_t)(D * es), (cuuint64_t)(T * D * es)};
