@@ -561,7 +561,9 @@ kdn_status kdn_linear_scan_step(const void* a, const void* b,
  *          were).  ldy is not read otherwise.
  * scale    [rows, ceil(D / 128)] fp32 device output, e4m3 only
  * eps      >= 0, finite
- * Sums in fp32: |h| up to about 1e18.  rows >= 0 (0: nothing is done);
+ * Sums in fp32: |h| up to about 1e18, and where eps is zero or smaller than
+ * mean(h^2), from about 1e-18.  No output may overlap an input but as said.
+ * rows >= 0 (0: nothing is done);
  * 1 <= D <= 16384; pointers 16-byte aligned.  Errors: KDN_ERR_INVALID_ARG,
  * KDN_ERR_UNSUPPORTED, KDN_ERR_CUDA.
  * ---------------------------------------------------------------------- */

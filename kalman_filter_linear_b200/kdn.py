@@ -571,8 +571,9 @@ def _load_quick():
     lib()
     try:
         from . import _kdn_quick
-        why = None if _kdn_quick.torch_version == torch.__version__.partition('+')[0] else \
-            f'it was built against torch {_kdn_quick.torch_version}'
+        built = getattr(_kdn_quick, 'torch_version', 'of another build')
+        why = None if built == torch.__version__.partition('+')[0] else \
+            f'it was built against torch {built}'
     except ImportError as e:
         why = e
     if why is None:

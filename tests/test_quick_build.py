@@ -34,11 +34,12 @@ def test_the_module_knows_its_torch():
     assert kdn._load_quick().torch_version == torch.__version__.partition('+')[0]
 
 
-def test_a_module_of_another_torch_is_not_used(monkeypatch):
+@pytest.mark.parametrize("module", [types.SimpleNamespace(torch_version='1.0'),
+                                    types.SimpleNamespace()])   # (one from before it knew)
+def test_a_module_of_another_torch_is_not_used(monkeypatch, module):
     monkeypatch.setattr(kdn, '_quick', None)
-    monkeypatch.setattr(package, '_kdn_quick', types.SimpleNamespace(torch_version='1.0'),
-                        raising=False)
-    with pytest.warns(RuntimeWarning, match='torch 1.0'):
+    monkeypatch.setattr(package, '_kdn_quick', module, raising=False)
+    with pytest.warns(RuntimeWarning, match='built against torch'):
         assert kdn._load_quick() is kdn._NoQuick
     with pytest.raises(TypeError, match='CUDA tensor'):
         kdn.kdn_linear_scan_step(torch.zeros(2, 4), torch.zeros(2, 4), torch.zeros(2, 4))
